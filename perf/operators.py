@@ -141,7 +141,8 @@ def _rounded(x):
     """x (fp32) as its block codes stand for it: E4M3 values times their block's scale."""
     K = x.shape[-1]
     b = torch.nn.functional.pad(x, (0, -K % B)).unflatten(-1, (-1, B))
-    s = b.abs().amax(-1, keepdim=True) / 448.0
+    a = b.abs().amax(-1, keepdim=True)
+    s = a / torch.full_like(a, 448.0)  # (a Python number as divisor would be a product with its reciprocal)
     q = (b / torch.where(s > 0, s, 1.0)).to(torch.float8_e4m3fn).float()
     return (q * s).flatten(-2)[..., :K]
 
@@ -250,7 +251,7 @@ def _codes64(x):
     out = torch.empty_like(x)
     for lo in range(0, x.shape[1], B):
         part = x[:, lo:lo + B]
-        s = (part.abs().max(1, keepdim=True).values.float() / 448).double()
+        s = (part.abs().max(1, keepdim=True).values / 448).float().double()
         q = (part / s.masked_fill(s == 0, 1)).float()
         # nearest E4M3 value: steps of 2^(e-3), no finer than 2^-9
         step = torch.ldexp(torch.ones_like(q), torch.frexp(q).exponent.clamp_min(-5) - 4)
