@@ -385,6 +385,125 @@ sq_status sq_select_outliers(const void *Xc, int64_t Mc, int64_t K, int64_t ldx,
                              int64_t nO, int64_t group, int32_t *O, double *scores,
                              void *workspace, size_t ws_bytes, sq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Block-scaled FP8 (no outlier channels).
+ *
+ *   Y[m,n] = bf16_rn( sum_b s_x[m,b] * s_w[n/128,b] * sum_{k in block b} e(X)[m,k] * e(W)[n,k] )
+ *
+ *   - Blocks: 128 consecutive channels of a token (X), 128 x 128 entries of the
+ *     weights (W); the last ones may be partial.
+ *   - s = a / 448 (fp32, IEEE), a = the block's absolute maximum; a == 0 gives
+ *     s = 0 and all-zero codes.  e(x) = the E4M3 code nearest to the fp32
+ *     quotient x / s, ties to the even code, the sign kept.
+ *   - Codes: u8 [rows, k_pad], k_pad = sq_k_pad_fp8b(K), zero bytes past K.
+ *     Scales: f32 [rows, s_ld] for X, [ceil(N / 128), s_ld] for W, s_ld =
+ *     sq_scale_ld_fp8b(K), zero past block ceil(K / 128) - 1.
+ *   - The products of a block run on the tensor cores (E4M3 x E4M3, fp32
+ *     accumulation) and are added to the fp32 sum with their scales; Y is
+ *     rounded once.
+ *   - Limits: K a multiple of 8 in [8, SQ_MAX_K], N a multiple of 8.
+ * Inputs are finite.  Every call is asynchronous, sq_prepare_weights_fp8b too.
+ * ------------------------------------------------------------------------ */
+int64_t sq_k_pad_fp8b(int64_t K);     /* roundup(K, 128) codes         */
+int64_t sq_scale_ld_fp8b(int64_t K);  /* roundup(K, 512) / 128 scales  */
+
+/* G weight matrices N x K: matrix g at W + g * stride_g (elements), rows ldw
+ * apart.  W_8 [G, N, k_pad], s_w [G, ceil(N / 128), s_ld]. */
+sq_status sq_prepare_weights_fp8b(const void *W, int64_t G, int64_t N, int64_t K, int64_t ldw, int64_t stride_g,
+                                  void *W_8, float *s_w, sq_stream_t stream);
+
+sq_status sq_quant_fp8b(const void *X, int64_t M, int64_t K, int64_t ldx, void *X_8, float *s_x, sq_stream_t stream);
+
+sq_status sq_gemm_fp8b(const void *X_8, const float *s_x, const void *W_8, const float *s_w,
+                       int64_t M, int64_t N, int64_t K, void *Y, int64_t ldy, sq_stream_t stream);
+
+/* Workspace of sq_linear_fp8b: codes and scales of X, each 256-byte aligned. */
+size_t sq_linear_workspace_bytes_fp8b(int64_t M, int64_t K);
+
+sq_status sq_linear_fp8b(const void *X, int64_t M, int64_t K, int64_t ldx, const void *W_8, const float *s_w, int64_t N,
+                         void *Y, int64_t ldy, void *workspace, size_t ws_bytes, sq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Mixture of experts: routing, and the experts' MLPs in block-scaled FP8.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The k experts of each token.  p = softmax (sigmoid == 0) or sigmoid of the
+ * token's E logits; an expert's score is p + bias[e] (p without a bias).  With
+ * groups > 1 the experts form `groups` equal runs; a group counts the sum of
+ * its group_top (1 or 2) best scores, and only the keep_groups best groups stay
+ * open.  The k best scores among the open groups are chosen, best first; ties
+ * (of groups too) go to the lower index, and scores are ordered as in 64 bits.
+ * weights = p of the chosen (without the bias), divided by their sum + 1e-20 if
+ * renorm, times scale.
+ *   A logit of -inf or NaN is never chosen (+inf counts as the largest finite
+ * fp32 value); where fewer than k remain the ids are -1 with weight 0.
+ *
+ *   logits  dev f32 (logits_bf16 == 0) or bf16 [T, ldl], ldl >= E
+ *   bias    dev f32 [E] or NULL
+ *   ids     dev i32 [T, k];  weights dev f32 [T, k]
+ * Limits: E <= 512, k <= 16 and at most the experts of keep_groups groups,
+ * groups <= 32 dividing E.
+ */
+sq_status sq_route(const void *logits, int logits_bf16, int64_t T, int64_t E, int64_t ldl, const float *bias, int sigmoid,
+                   int64_t groups, int64_t keep_groups, int64_t group_top, int64_t k, int renorm, float scale,
+                   int32_t *ids, float *weights, sq_stream_t stream);
+
+/*
+ * Rows of the T * k (token, choice) pairs, ordered by expert and inside an
+ * expert by pair: pos [T, k] = the pair's row (-1 where ids holds no expert of
+ * [0, E)); offsets [E + 1]: expert e has rows [offsets[e], offsets[e + 1]).
+ */
+sq_status sq_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t E, int32_t *offsets, int32_t *pos,
+                          sq_stream_t stream);
+
+/* sq_quant_fp8b of the T tokens, each written to its rows pos[t, 0 .. k - 1] of
+ * X_8 [T * k, k_pad] and s_x [T * k, s_ld].  Other rows stay as they were; a
+ * token without a row is not read. */
+sq_status sq_moe_quant_fp8b(const void *X, int64_t T, int64_t K, int64_t ldx, const int32_t *pos, int64_t k,
+                            void *X_8, float *s_x, sq_stream_t stream);
+
+/*
+ * First half of the experts' MLPs: for the rows of expert e,
+ *   h = silu(x G_e^T) * (x U_e^T)   (products as sq_gemm_fp8b, fp32)
+ * quantized as by sq_quant_fp8b straight from fp32 (no rounding to bf16).
+ *   W13_8 [E, 2, I, k_pad], s_w13 [E, 2, ceil(I / 128), s_ld]: G_e, then U_e
+ *   H_8 [R, sq_k_pad_fp8b(I)], s_h [R, sq_scale_ld_fp8b(I)]
+ * R: rows of X_8 and H_8 (at least offsets[E]); rows from offsets[E] on stay as
+ * they were.
+ */
+sq_status sq_moe_swiglu_fp8b(const void *X_8, const float *s_x, const int32_t *offsets, int64_t R,
+                             const void *W13_8, const float *s_w13, int64_t E, int64_t I, int64_t K,
+                             void *H_8, float *s_h, sq_stream_t stream);
+
+/* sq_gemm_fp8b with one weight matrix per expert: rows [offsets[e],
+ * offsets[e + 1]) take W_8[e].  Rows of Y [R, ldy] from offsets[E] on stay as
+ * they were. */
+sq_status sq_moe_gemm_fp8b(const void *X_8, const float *s_x, const int32_t *offsets, int64_t R,
+                           const void *W_8, const float *s_w, int64_t E, int64_t N, int64_t K,
+                           void *Y, int64_t ldy, sq_stream_t stream);
+
+/* Y[t] = bf16_rn( sum_j weights[t,j] * Z[pos[t,j]] ), fp32, in the order of j;
+ * entries of pos outside [0, R) add nothing (a token without any gets 0). */
+sq_status sq_moe_combine(const void *Z, int64_t R, int64_t ldz, const int32_t *pos, const float *weights,
+                         int64_t T, int64_t k, int64_t N, void *Y, int64_t ldy, sq_stream_t stream);
+
+/* Workspace of sq_experts_fp8b (0 for T == 0). */
+size_t sq_experts_workspace_bytes_fp8b(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
+
+/*
+ * The experts' MLPs of T tokens: sq_moe_dispatch, sq_moe_quant_fp8b,
+ * sq_moe_swiglu_fp8b, sq_moe_gemm_fp8b (the experts' outputs in bf16) and
+ * sq_moe_combine on one stream.
+ *   X [T, ldx] bf16, ids and weights [T, k] as from sq_route
+ *   W13_8 [E, 2, I, sq_k_pad_fp8b(H)], W2_8 [E, H, sq_k_pad_fp8b(I)]
+ *   Y [T, ldy] bf16
+ */
+sq_status sq_experts_fp8b(const void *X, int64_t T, int64_t H, int64_t ldx, const int32_t *ids, const float *weights,
+                          int64_t k, const void *W13_8, const float *s_w13, const void *W2_8, const float *s_w2,
+                          int64_t E, int64_t I, void *Y, int64_t ldy, void *workspace, size_t ws_bytes,
+                          sq_stream_t stream);
+
 /*
  * Waits for `stream`, then reports (and clears) the device error word of the
  * current device: SQ_ERR_TIMEOUT if a kernel's bounded wait ran out,

@@ -19,9 +19,14 @@ write-up of arXiv:2512.05409, sections 5 and 9 -- static mask chosen offline,
 symmetric quantization, weight columns reordered by the mask.  Two more low
 paths keep the same split: FP8 E4M3 (OSC's fallback for the inputs of W2)
 and MXFP4 (OSC abstract: the split fits 4-bit micro-scaling hardware).
+
+Beside the dual-path layer: plain FP8 layers with one scale per 128 channels
+of a token and per 128 x 128 weights (``SQBlockLinear``), and mixtures of such
+experts with their routing (``route``, ``SQExperts``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -43,6 +48,12 @@ __all__ = [
     "PreparedSQF", "prepare_weights_sqf", "quant_gather_sqf", "gemm_sqf",
     "sq_select_outliers_workspace_bytes", "sq_select_outliers", "select_outliers",
     "PreparedWeights", "prepare_weights", "quant_gather", "gemm", "SQLinear",
+    "sq_k_pad_fp8b", "sq_scale_ld_fp8b", "sq_linear_workspace_bytes_fp8b", "sq_experts_workspace_bytes_fp8b",
+    "sq_prepare_weights_fp8b", "sq_quant_fp8b", "sq_gemm_fp8b", "sq_linear_fp8b",
+    "sq_route", "sq_moe_dispatch", "sq_moe_quant_fp8b", "sq_moe_swiglu_fp8b", "sq_moe_gemm_fp8b", "sq_moe_combine",
+    "sq_experts_fp8b",
+    "PreparedFP8B", "prepare_weights_fp8b", "quant_fp8b", "linear_fp8b", "SQBlockLinear",
+    "route", "experts_fp8b", "SQExperts",
 ]
 
 SQ_OK = 0
@@ -128,6 +139,29 @@ def load():
     lib.sq_select_outliers_workspace_bytes.argtypes = [I, I, I, I]
     lib.sq_select_outliers_workspace_bytes.restype = Z
     lib.sq_select_outliers.argtypes = [P, I, I, I, P, I, I, I, I, P, P, P, Z, P]
+    lib.sq_k_pad_fp8b.argtypes = [I]
+    lib.sq_k_pad_fp8b.restype = I
+    lib.sq_scale_ld_fp8b.argtypes = [I]
+    lib.sq_scale_ld_fp8b.restype = I
+    lib.sq_linear_workspace_bytes_fp8b.argtypes = [I, I]
+    lib.sq_linear_workspace_bytes_fp8b.restype = Z
+    lib.sq_experts_workspace_bytes_fp8b.argtypes = [I, I, I, I, I]
+    lib.sq_experts_workspace_bytes_fp8b.restype = Z
+    lib.sq_prepare_weights_fp8b.argtypes = [P, I, I, I, I, I, P, P, P]
+    lib.sq_quant_fp8b.argtypes = [P, I, I, I, P, P, P]
+    lib.sq_gemm_fp8b.argtypes = [P, P, P, P, I, I, I, P, I, P]
+    lib.sq_linear_fp8b.argtypes = [P, I, I, I, P, P, I, P, I, P, Z, P]
+    lib.sq_route.argtypes = [P, C, I, I, I, P, C, I, I, I, I, C, ctypes.c_float, P, P, P]
+    lib.sq_moe_dispatch.argtypes = [P, I, I, I, P, P, P]
+    lib.sq_moe_quant_fp8b.argtypes = [P, I, I, I, P, I, P, P, P]
+    lib.sq_moe_swiglu_fp8b.argtypes = [P, P, P, I, P, P, I, I, I, P, P, P]
+    lib.sq_moe_gemm_fp8b.argtypes = [P, P, P, I, P, P, I, I, I, P, I, P]
+    lib.sq_moe_combine.argtypes = [P, I, I, P, P, I, I, I, P, I, P]
+    lib.sq_experts_fp8b.argtypes = [P, I, I, I, P, P, I, P, P, P, P, I, I, P, I, P, Z, P]
+    for f in (lib.sq_prepare_weights_fp8b, lib.sq_quant_fp8b, lib.sq_gemm_fp8b, lib.sq_linear_fp8b, lib.sq_route,
+              lib.sq_moe_dispatch, lib.sq_moe_quant_fp8b, lib.sq_moe_swiglu_fp8b, lib.sq_moe_gemm_fp8b,
+              lib.sq_moe_combine, lib.sq_experts_fp8b):
+        f.restype = F
     for f in (lib.sq_prepare_weights, lib.sq_quant_gather, lib.sq_gemm, lib.sq_linear, lib.sq_check,
               lib.sq_selftest_watchdog, lib.sq_linear_noalloc, lib.sq_prepare_weights_fp8, lib.sq_quant_gather_fp8,
               lib.sq_gemm_fp8, lib.sq_linear_fp8, lib.sq_select_outliers, lib.sq_prepare_weights_mx,
@@ -421,6 +455,204 @@ def sq_select_outliers(Xc: torch.Tensor, W: torch.Tensor, nO: int, group: int, O
     _raise(st, "sq_select_outliers")
 
 
+# Block-scaled FP8: E4M3 codes u8 [rows, sq_k_pad_fp8b(K)], fp32 scales per 128
+# channels [rows, sq_scale_ld_fp8b(K)] (weights: per 128 x 128 block).
+def _block_device(*tensors) -> None:
+    """The calls below launch on the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.numel() and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a matrix; a single row has none that matters."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _expect(t: torch.Tensor, name: str, dtype, *shape) -> None:
+    """A contiguous tensor of this type and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+
+
+def sq_k_pad_fp8b(K: int) -> int:
+    return int(load().sq_k_pad_fp8b(K))
+
+
+def sq_scale_ld_fp8b(K: int) -> int:
+    return int(load().sq_scale_ld_fp8b(K))
+
+
+def sq_linear_workspace_bytes_fp8b(M: int, K: int) -> int:
+    return int(load().sq_linear_workspace_bytes_fp8b(M, K))
+
+
+def sq_experts_workspace_bytes_fp8b(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(load().sq_experts_workspace_bytes_fp8b(T, k, E, H, I))
+
+
+def sq_prepare_weights_fp8b(W: torch.Tensor, W_8: torch.Tensor, s_w: torch.Tensor, stream=None) -> None:
+    """Codes and scales of W [N, K] or of the matrices W [..., N, K] (bf16, unit inner stride)."""
+    if W.dtype != torch.bfloat16:
+        raise TypeError(f"W: expected {torch.bfloat16}, got {W.dtype}")
+    N, K = W.shape[-2:]
+    W3 = W.unsqueeze(0) if W.dim() == 2 else W if W.dim() == 3 else W.flatten(0, -3)
+    if W3.stride(2) != 1:
+        raise ValueError("W: expected unit inner stride")
+    G = W3.shape[0]
+    _expect(W_8, "W_8", torch.uint8, *W.shape[:-1], sq_k_pad_fp8b(K))
+    _expect(s_w, "s_w", torch.float32, *W.shape[:-2], -(-N // 128), sq_scale_ld_fp8b(K))
+    _block_device(W, W_8, s_w)
+    st = load().sq_prepare_weights_fp8b(_ptr(W3), G, N, K, W3.stride(1), W3.stride(0), _ptr(W_8), _ptr(s_w),
+                                        _stream(stream))
+    _raise(st, "sq_prepare_weights_fp8b")
+
+
+def sq_quant_fp8b(X: torch.Tensor, X_8: torch.Tensor, s_x: torch.Tensor, stream=None) -> None:
+    _rowmajor(X, "X", torch.bfloat16)
+    M, K = X.shape
+    _expect(X_8, "X_8", torch.uint8, M, sq_k_pad_fp8b(K))
+    _expect(s_x, "s_x", torch.float32, M, sq_scale_ld_fp8b(K))
+    _block_device(X, X_8, s_x)
+    _raise(load().sq_quant_fp8b(_ptr(X), M, K, _ld(X), _ptr(X_8), _ptr(s_x), _stream(stream)), "sq_quant_fp8b")
+
+
+def _check_codes(c: torch.Tensor, s: torch.Tensor, names, rows, K: int, scale_rows) -> None:
+    _expect(c, names[0], torch.uint8, *rows, sq_k_pad_fp8b(K))
+    _expect(s, names[1], torch.float32, *scale_rows, sq_scale_ld_fp8b(K))
+
+
+def sq_gemm_fp8b(X_8, s_x, W_8, s_w, M: int, N: int, K: int, Y: torch.Tensor, stream=None) -> None:
+    _rowmajor(Y, "Y", torch.bfloat16)
+    if tuple(Y.shape) != (M, N):
+        raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
+    _check_codes(X_8, s_x, ("X_8", "s_x"), (M,), K, (M,))
+    _check_codes(W_8, s_w, ("W_8", "s_w"), (N,), K, (-(-N // 128),))
+    _block_device(X_8, s_x, W_8, s_w, Y)
+    st = load().sq_gemm_fp8b(_ptr(X_8), _ptr(s_x), _ptr(W_8), _ptr(s_w), M, N, K, _ptr(Y), _ld(Y), _stream(stream))
+    _raise(st, "sq_gemm_fp8b")
+
+
+def sq_linear_fp8b(X: torch.Tensor, W_8, s_w, N: int, Y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    _rowmajor(X, "X", torch.bfloat16)
+    _rowmajor(Y, "Y", torch.bfloat16)
+    M, K = X.shape
+    if tuple(Y.shape) != (M, N):
+        raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
+    _check_codes(W_8, s_w, ("W_8", "s_w"), (N,), K, (-(-N // 128),))
+    _block_device(X, W_8, s_w, Y, workspace)
+    st = load().sq_linear_fp8b(_ptr(X), M, K, _ld(X), _ptr(W_8), _ptr(s_w), N, _ptr(Y), _ld(Y),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _raise(st, "sq_linear_fp8b")
+
+
+# Mixture of experts: routing, dispatch, the experts' products, combination.
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def sq_route(logits: torch.Tensor, k: int, ids: torch.Tensor, weights: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, scoring: str = "softmax", groups: int = 1, keep_groups: int = 1,
+             group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    _rowmajor(logits, "logits")
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring: expected one of {sorted(_SCORING)}, got {scoring!r}")
+    T, E = logits.shape
+    _expect(ids, "ids", torch.int32, T, k)
+    _expect(weights, "weights", torch.float32, T, k)
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, E)
+    _block_device(logits, bias, ids, weights)
+    st = load().sq_route(_ptr(logits), int(logits.dtype == torch.bfloat16), T, E, _ld(logits), _ptr(bias),
+                         _SCORING[scoring], groups, keep_groups, group_top, k, int(renormalize), float(scale),
+                         _ptr(ids), _ptr(weights), _stream(stream))
+    _raise(st, "sq_route")
+
+
+def sq_moe_dispatch(ids: torch.Tensor, E: int, offsets: torch.Tensor, pos: torch.Tensor, stream=None) -> None:
+    T, k = ids.shape
+    _expect(ids, "ids", torch.int32, T, k)
+    _expect(offsets, "offsets", torch.int32, E + 1)
+    _expect(pos, "pos", torch.int32, T, k)
+    _block_device(ids, offsets, pos)
+    _raise(load().sq_moe_dispatch(_ptr(ids), T, k, E, _ptr(offsets), _ptr(pos), _stream(stream)), "sq_moe_dispatch")
+
+
+def sq_moe_quant_fp8b(X: torch.Tensor, pos: torch.Tensor, X_8: torch.Tensor, s_x: torch.Tensor, stream=None) -> None:
+    _rowmajor(X, "X", torch.bfloat16)
+    T, K = X.shape
+    k = pos.shape[1]
+    _expect(pos, "pos", torch.int32, T, k)
+    _check_codes(X_8, s_x, ("X_8", "s_x"), (T * k,), K, (T * k,))
+    _block_device(X, pos, X_8, s_x)
+    st = load().sq_moe_quant_fp8b(_ptr(X), T, K, _ld(X), _ptr(pos), k, _ptr(X_8), _ptr(s_x), _stream(stream))
+    _raise(st, "sq_moe_quant_fp8b")
+
+
+def sq_moe_swiglu_fp8b(X_8, s_x, offsets, W13_8, s_w13, I: int, K: int, H_8, s_h, stream=None) -> None:
+    R, E = X_8.shape[0], offsets.numel() - 1
+    _expect(offsets, "offsets", torch.int32, E + 1)
+    _check_codes(X_8, s_x, ("X_8", "s_x"), (R,), K, (R,))
+    _check_codes(W13_8, s_w13, ("W13_8", "s_w13"), (E, 2, I), K, (E, 2, -(-I // 128)))
+    _check_codes(H_8, s_h, ("H_8", "s_h"), (R,), I, (R,))
+    _block_device(X_8, s_x, offsets, W13_8, s_w13, H_8, s_h)
+    st = load().sq_moe_swiglu_fp8b(_ptr(X_8), _ptr(s_x), _ptr(offsets), R, _ptr(W13_8), _ptr(s_w13), E, I, K,
+                                   _ptr(H_8), _ptr(s_h), _stream(stream))
+    _raise(st, "sq_moe_swiglu_fp8b")
+
+
+def sq_moe_gemm_fp8b(X_8, s_x, offsets, W_8, s_w, N: int, K: int, Y: torch.Tensor, stream=None) -> None:
+    _rowmajor(Y, "Y", torch.bfloat16)
+    R, E = X_8.shape[0], offsets.numel() - 1
+    if tuple(Y.shape) != (R, N):
+        raise ValueError(f"Y: expected shape {(R, N)}, got {tuple(Y.shape)}")
+    _expect(offsets, "offsets", torch.int32, E + 1)
+    _check_codes(X_8, s_x, ("X_8", "s_x"), (R,), K, (R,))
+    _check_codes(W_8, s_w, ("W_8", "s_w"), (E, N), K, (E, -(-N // 128)))
+    _block_device(X_8, s_x, offsets, W_8, s_w, Y)
+    st = load().sq_moe_gemm_fp8b(_ptr(X_8), _ptr(s_x), _ptr(offsets), R, _ptr(W_8), _ptr(s_w), E, N, K, _ptr(Y),
+                                 _ld(Y), _stream(stream))
+    _raise(st, "sq_moe_gemm_fp8b")
+
+
+def sq_moe_combine(Z: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, Y: torch.Tensor, stream=None) -> None:
+    _rowmajor(Z, "Z", torch.bfloat16)
+    _rowmajor(Y, "Y", torch.bfloat16)
+    T, k = pos.shape
+    N = Z.shape[1]
+    if tuple(Y.shape) != (T, N):
+        raise ValueError(f"Y: expected shape {(T, N)}, got {tuple(Y.shape)}")
+    _expect(pos, "pos", torch.int32, T, k)
+    _expect(weights, "weights", torch.float32, T, k)
+    _block_device(Z, pos, weights, Y)
+    st = load().sq_moe_combine(_ptr(Z), Z.shape[0], _ld(Z), _ptr(pos), _ptr(weights), T, k, N, _ptr(Y),
+                               _ld(Y), _stream(stream))
+    _raise(st, "sq_moe_combine")
+
+
+def sq_experts_fp8b(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13_8, s_w13, W2_8, s_w2, I: int,
+                    Y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    _rowmajor(X, "X", torch.bfloat16)
+    _rowmajor(Y, "Y", torch.bfloat16)
+    T, H = X.shape
+    E, k = W2_8.shape[0], ids.shape[1]
+    if tuple(Y.shape) != (T, H):
+        raise ValueError(f"Y: expected shape {(T, H)}, got {tuple(Y.shape)}")
+    _expect(ids, "ids", torch.int32, T, k)
+    _expect(weights, "weights", torch.float32, T, k)
+    _check_codes(W13_8, s_w13, ("W13_8", "s_w13"), (E, 2, I), H, (E, 2, -(-I // 128)))
+    _check_codes(W2_8, s_w2, ("W2_8", "s_w2"), (E, H), I, (E, -(-H // 128)))
+    _block_device(X, ids, weights, W13_8, s_w13, W2_8, s_w2, Y, workspace)
+    st = load().sq_experts_fp8b(_ptr(X), T, H, _ld(X), _ptr(ids), _ptr(weights), k, _ptr(W13_8), _ptr(s_w13),
+                                _ptr(W2_8), _ptr(s_w2), E, I, _ptr(Y), _ld(Y), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _raise(st, "sq_experts_fp8b")
+
+
 def sq_check(stream=None) -> None:
     _raise(load().sq_check(_stream(stream)), "sq_check")
 
@@ -611,3 +843,148 @@ def gemm_sqf(X_N, s_x4, X_8, s_x8, pw: PreparedSQF, Y: Optional[torch.Tensor] = 
     acc = torch.empty(M, pw.N, dtype=torch.int32, device=dev) if debug else None
     sq_gemm_sqf(X_N, s_x4, X_8, s_x8, pw.W_N, pw.s_lo, pw.W_H, pw.W_E, pw.s_hi, M, pw.N, pw.K, Y, P, acc, stream)
     return (Y, acc, P) if debug else Y
+
+
+# ----------------------------------------------------------------- block-scaled FP8 layers, mixture of experts
+@contextlib.contextmanager
+def _scope(dev: torch.device, stream):
+    """Makes dev and the stream (None: dev's current one) current, so that buffers allocated inside belong to it."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
+
+
+def _here(dev: torch.device, stream) -> bool:
+    return stream is None and dev.index == torch.cuda.current_device()
+
+
+@dataclasses.dataclass
+class PreparedFP8B:
+    """Block-scaled FP8 weights (see sq_prepare_weights_fp8b): one matrix, or a stack of them
+    (leading dimensions of W_8 and s_w)."""
+    N: int
+    K: int
+    W_8: torch.Tensor        # uint8 [..., N, sq_k_pad_fp8b(K)]
+    s_w: torch.Tensor        # float32 [..., ceil(N / 128), sq_scale_ld_fp8b(K)]
+
+    def state_dict(self) -> dict:
+        return {"N": self.N, "K": self.K, "W_8": self.W_8, "s_w": self.s_w}
+
+    @classmethod
+    def from_state_dict(cls, d: dict, device=None) -> "PreparedFP8B":
+        mv = (lambda t: t.to(device)) if device is not None else (lambda t: t)
+        return cls(int(d["N"]), int(d["K"]), mv(d["W_8"]), mv(d["s_w"]))
+
+
+def prepare_weights_fp8b(W: torch.Tensor, stream=None) -> PreparedFP8B:
+    """Block-scaled FP8 form of the bf16 weights W [..., N, K] on the GPU."""
+    if not _here(W.device, stream):
+        with _scope(W.device, stream):
+            return prepare_weights_fp8b(W)
+    N, K = W.shape[-2:]
+    W_8 = torch.empty(*W.shape[:-1], sq_k_pad_fp8b(K), dtype=torch.uint8, device=W.device)
+    s_w = torch.empty(*W.shape[:-2], -(-N // 128), sq_scale_ld_fp8b(K), dtype=torch.float32, device=W.device)
+    sq_prepare_weights_fp8b(W, W_8, s_w)
+    return PreparedFP8B(N, K, W_8, s_w)
+
+
+def quant_fp8b(X: torch.Tensor, stream=None):
+    """(codes uint8 [M, sq_k_pad_fp8b(K)], scales float32 [M, sq_scale_ld_fp8b(K)]) of bf16 x [M, K]."""
+    if not _here(X.device, stream):
+        with _scope(X.device, stream):
+            return quant_fp8b(X)
+    M, K = X.shape
+    X_8 = torch.empty(M, sq_k_pad_fp8b(K), dtype=torch.uint8, device=X.device)
+    s_x = torch.empty(M, sq_scale_ld_fp8b(K), dtype=torch.float32, device=X.device)
+    sq_quant_fp8b(X, X_8, s_x)
+    return X_8, s_x
+
+
+def linear_fp8b(X: torch.Tensor, pw: PreparedFP8B, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x W^T for bf16 x [M, K] and one block-scaled matrix; x is quantized on the way.
+
+    The workspace is allocated per call on the stream, so calls on several streams and captured graphs share none."""
+    if not _here(X.device, stream):
+        with _scope(X.device, stream):
+            return linear_fp8b(X, pw, out)
+    _rowmajor(X, "X", torch.bfloat16)
+    M, K = X.shape
+    if K != pw.K:
+        raise ValueError(f"X: expected {pw.K} channels, got {K}")
+    if out is None:
+        out = torch.empty(M, pw.N, dtype=torch.bfloat16, device=X.device)
+    ws = torch.empty(sq_linear_workspace_bytes_fp8b(M, K), dtype=torch.uint8, device=X.device)
+    sq_linear_fp8b(X, pw.W_8, pw.s_w, pw.N, out, ws)
+    return out
+
+
+class SQBlockLinear:
+    """A linear layer in block-scaled FP8: ``y = layer(x)`` for bf16 x [M, K] on the GPU."""
+
+    def __init__(self, W: torch.Tensor, stream=None):
+        if W.dim() != 2:
+            raise ValueError("W: expected a matrix [N, K]")
+        self.weights = prepare_weights_fp8b(W, stream)
+
+    def __call__(self, X: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        return linear_fp8b(X, self.weights, out, stream)
+
+
+def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, scoring: str = "softmax",
+          groups: int = 1, keep_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+          stream=None):
+    """(ids int32 [T, k], weights float32 [T, k]): the experts of each token from its router logits
+    [T, E] (float32 or bfloat16); see sq_route in include/sq.h."""
+    dev = logits.device
+    if not _here(dev, stream):
+        with _scope(dev, stream):
+            return route(logits, k, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
+    T = logits.shape[0]
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+    sq_route(logits, k, ids, weights, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
+    return ids, weights
+
+
+def experts_fp8b(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: PreparedFP8B, down: PreparedFP8B,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [T, H] = sum_j weights[:, j] * mlp_{ids[:, j]}(x), mlp(x) = (silu(x G^T) * (x U^T)) D^T, for bf16 x [T, H].
+
+    gate_up holds G and U stacked [E, 2, I, H], down holds D [E, H, I].  Index -1 adds nothing."""
+    if not _here(X.device, stream):
+        with _scope(X.device, stream):
+            return experts_fp8b(X, ids, weights, gate_up, down, out)
+    _rowmajor(X, "X", torch.bfloat16)
+    T, H = X.shape
+    I = gate_up.N
+    if gate_up.K != H or down.N != H or down.K != I:
+        raise ValueError(f"X [.., {H}], gate_up {gate_up.N} x {gate_up.K} and down {down.N} x {down.K} do not fit together")
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=X.device)
+    ws = torch.empty(sq_experts_workspace_bytes_fp8b(T, ids.shape[1], down.W_8.shape[0], H, I), dtype=torch.uint8,
+                     device=X.device)
+    sq_experts_fp8b(X, ids, weights, gate_up.W_8, gate_up.s_w, down.W_8, down.s_w, I, out, ws)
+    return out
+
+
+class SQExperts:
+    """A mixture of experts in block-scaled FP8: ``y = layer(x, logits)`` for bf16 x [T, H] and the router's
+    logits [T, E]; the routing arguments are those of ``route``."""
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, k: int, stream=None, **routing):
+        E, H, I = down.shape
+        if gate_up.numel() != 2 * E * I * H or gate_up.shape[0] != E or gate_up.shape[-1] != H:
+            raise ValueError(f"gate_up: expected [{E}, 2, {I}, {H}] or [{E}, {2 * I}, {H}], got {tuple(gate_up.shape)}")
+        self.k = k
+        self.routing = routing
+        with _scope(down.device, stream):
+            self.gate_up = prepare_weights_fp8b(gate_up.reshape(E, 2, I, H))
+            self.down = prepare_weights_fp8b(down)
+
+    def __call__(self, X: torch.Tensor, logits: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        if not _here(X.device, stream):
+            with _scope(X.device, stream):
+                return self(X, logits, out)
+        ids, weights = route(logits, self.k, **self.routing)
+        return experts_fp8b(X, ids, weights, self.gate_up, self.down, out)

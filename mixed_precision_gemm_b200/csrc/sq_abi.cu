@@ -7,8 +7,10 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
 #include <mutex>
 #include <type_traits>
 #include <string>
@@ -16,9 +18,11 @@
 
 #include "../../include/sq.h"
 #include "sq_device.cuh"
+#include "sq_fp8b.cuh"
 #include "sq_gemm_common.cuh"
 #include "sq_gemm_pair.cuh"
 #include "sq_gemm_skinny.cuh"
+#include "sq_moe.cuh"
 #include "sq_mxquant.cuh"
 #include "sq_rowquant.cuh"
 #include "sq_rowquant_stream.cuh"
@@ -1390,3 +1394,5 @@ extern "C" sq_status sq_linear_noalloc(const void *X, int64_t M, int64_t K, int6
     SQ_TRY(noalloc_scratch(&ws));
     return sq_linear(X, M, K, ldx, chan_tab, W_N, s_w, W_O, N, nO, Y, ldy, ws, SQ_NOALLOC_WS_BYTES, stream);
 }
+
+#include "sq_fp8b_host.cuh"

@@ -1,0 +1,309 @@
+// Block-scaled FP8: E4M3 codes with one fp32 scale for each 128 channels of a
+// token (X) or each 128 x 128 block of the weights (W).
+//
+//   s = fl(a / 448), a the block's largest magnitude; a == 0: s = 0, codes 0
+//   e(x) = the E4M3 code nearest to fl(x / s), ties to even
+//   Y[m,n] = sum_b sx[m,b] sw[n/128,b] sum_{k in block b} e(X)[m,k] e(W)[n,k]
+//
+// Storage: codes [rows, k_pad] bytes, k_pad = roundup(K, 128), zero past K;
+// scales [rows or row blocks, s_ld] floats, s_ld = roundup(K, 512) / 128, zero
+// past the last block (so a row's scales can be read four at a time).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "sq_device.cuh"
+#include "sq_rowquant.cuh"
+
+namespace sqb {
+
+constexpr int BLK = 128;        // channels (and weight rows) per scale
+constexpr float kTop = 448.0f;  // largest E4M3 magnitude
+
+// ---------------------------------------------------------------- quantizers
+// Scale of a block from the bits of its largest bf16 magnitude, and the
+// constants of the quotient (sq_rowquant.cuh: correctly rounded x / s).
+struct BlockScale {
+    float s;
+    bool zero, up;
+    sqq::RowScale rs;
+};
+
+__device__ __forceinline__ BlockScale block_scale(float amax)
+{
+    BlockScale b;
+    b.zero = amax == 0.0f;
+    b.s = b.zero ? 0.0f : __fdiv_rn(amax, kTop);
+    b.up = !b.zero && b.s < sqq::kTinyScale;
+    const float s1 = b.up ? b.s * sqq::kUpScale : b.s;
+    const float inv = b.zero ? 0.0f : __frcp_rn(s1);
+    b.rs.inv2 = sqq::f2_pack(__float_as_uint(inv), __float_as_uint(inv));
+    b.rs.negs2 = sqq::f2_pack(__float_as_uint(-s1), __float_as_uint(-s1));
+    b.rs.magic2 = 0;
+    b.rs.up2 = sqq::f2_pack(__float_as_uint(sqq::kUpScale), __float_as_uint(sqq::kUpScale));
+    return b;
+}
+
+__device__ __forceinline__ uint2 block_codes(const uint4 &v, const BlockScale &b)
+{
+    uint2 c = make_uint2(0u, 0u);
+    if (b.zero) return c;
+    if (!b.up) sqq::quant8_fp8_pairs<false>(v, b.rs, c.x, c.y);
+    else sqq::quant8_fp8_pairs<true>(v, b.rs, c.x, c.y);
+    return c;
+}
+
+// Largest magnitude of 8 bf16 values, as bf16 bits.
+__device__ __forceinline__ uint32_t absmax8(const uint4 &v)
+{
+    const uint32_t m = sqq::maxabs_bf16x2(sqq::maxabs_bf16x2(v.x, v.y), sqq::maxabs_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+constexpr int QB_THREADS = 256;
+constexpr int QB_CHUNKS = 4;                     // 8-channel chunks per lane
+constexpr int QB_SEG = 32 * QB_CHUNKS * 8;       // channels per warp task
+
+// Codes and scales of the rows of X.  One warp takes 1024 channels of a row:
+// lane l holds chunks l, l + 32, ... of 8 channels (16 bytes), so 16 lanes
+// share a block of 128 and its maximum takes four shuffles.
+// With pos (top > 0) row t of X goes to the `top` rows pos[t * top + j] of the
+// outputs (entries outside [0, rows_out) are skipped): one read of a token for all
+// of its experts' copies; a token without any is not read.
+// Memory-bound: 2 K bytes read and (K + 4 K / 128) written per output row.
+__global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__restrict__ X, int64_t rows, int K, int64_t ldx,
+                                                           int k_pad, int s_ld, const int32_t *__restrict__ pos, int top,
+                                                           int64_t rows_out, uint8_t *__restrict__ X_8,
+                                                           float *__restrict__ s_x)
+{
+    sqd::pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int segs = (s_ld * BLK + QB_SEG - 1) / QB_SEG;
+    const int64_t tasks = rows * segs;
+    const int64_t wpg = static_cast<int64_t>(gridDim.x) * (QB_THREADS / 32);
+    sqd::pdl_wait();
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (QB_THREADS / 32) + (threadIdx.x >> 5); w < tasks; w += wpg) {
+        const int64_t r = w / segs;
+        const int c0 = static_cast<int>(w - r * segs) * (QB_SEG / 8) + lane;
+        if (top > 0) {
+            bool any = false;
+            for (int j = 0; j < top; ++j) any |= pos[r * top + j] >= 0;
+            if (!any) continue;
+        }
+        const uint16_t *row = X + r * ldx;
+        uint4 v[QB_CHUNKS];
+#pragma unroll
+        for (int i = 0; i < QB_CHUNKS; ++i) {
+            const int c = c0 + 32 * i;
+            v[i] = c < (K >> 3) ? sqd::ld_nc_v4(row + 8 * c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < QB_CHUNKS; ++i) {
+            const int c = c0 + 32 * i;
+            uint32_t m = absmax8(v[i]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const BlockScale b = block_scale(__uint_as_float(m << 16));
+            const uint2 q = block_codes(v[i], b);
+            const int n = top > 0 ? top : 1;
+            for (int j = 0; j < n; ++j) {
+                const int64_t d = top > 0 ? pos[r * top + j] : r;
+                if (d < 0 || d >= rows_out) continue;
+                if (8 * c < k_pad) *reinterpret_cast<uint2 *>(X_8 + d * k_pad + 8 * c) = q;
+                if ((lane & 15) == 0 && (c >> 4) < s_ld) s_x[d * s_ld + (c >> 4)] = b.s;
+            }
+        }
+    }
+}
+
+// Codes and scales of weight blocks: CTA (kb, nb, g) takes the 128 x 128 block
+// (nb, kb) of matrix g.  Thread t holds chunk t % 16 of rows t / 16, + 16, ...
+// The blocks past the last one of a scale row (kb up to s_ld) only write their 0.
+__global__ void __launch_bounds__(256) weight_blocks_kernel(const uint16_t *__restrict__ W, int N, int K, int64_t ldw,
+                                                            int64_t stride_g, int k_pad, int s_ld,
+                                                            uint8_t *__restrict__ W_8, float *__restrict__ s_w)
+{
+    __shared__ uint32_t red[8];
+    sqd::pdl_launch_dependents();
+    const int kb = blockIdx.x, nb = blockIdx.y;
+    const int64_t g = blockIdx.z;
+    const int c = kb * 16 + (threadIdx.x & 15);
+    const int r0 = nb * BLK + (threadIdx.x >> 4);
+    sqd::pdl_wait();
+    uint4 v[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        v[i] = (r < N && c < (K >> 3)) ? sqd::ld_nc_v4(W + g * stride_g + r * ldw + 8 * c) : make_uint4(0, 0, 0, 0);
+        m = max(m, absmax8(v[i]));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+    const BlockScale b = block_scale(__uint_as_float(m << 16));
+    if (threadIdx.x == 0) s_w[(g * gridDim.y + nb) * s_ld + kb] = b.s;
+    if (8 * c >= k_pad) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < N) *reinterpret_cast<uint2 *>(W_8 + (g * N + r) * k_pad + 8 * c) = block_codes(v[i], b);
+    }
+}
+
+// ---------------------------------------------------------------- products
+// One product, or one per expert: rows [offsets[g], offsets[g + 1]) of X take
+// matrix g.  Without offsets, one matrix takes rows [0, M).
+struct ProductArgs {
+    const uint8_t *X_8;
+    const float *s_x;
+    const uint8_t *W_8;      // [G, (2,) N, k_pad]
+    const float *s_w;        // [G, (2,) nb, s_ld]
+    const int32_t *offsets;  // [G + 1], or NULL
+    int64_t M;               // rows of X_8 (capacity where there are offsets)
+    int G, N, kb, k_pad, s_ld, nb;
+    uint16_t *Y;             // bf16 [M, ldy]
+    int64_t ldy;
+    uint8_t *H_8;            // SwiGLU form: codes [M, h_pad] and scales [M, h_ld]
+    float *s_h;
+    int h_pad, h_ld;
+};
+
+// Rows of expert g, clamped to the buffers whatever the offsets hold.
+__device__ __forceinline__ void expert_rows(const ProductArgs &a, int g, int64_t &lo, int64_t &hi)
+{
+    if (!a.offsets) {
+        lo = 0;
+        hi = a.M;
+        return;
+    }
+    lo = min(max(static_cast<int64_t>(a.offsets[g]), int64_t(0)), a.M);
+    hi = min(max(static_cast<int64_t>(a.offsets[g + 1]), lo), a.M);
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+constexpr int SP_BM = 32, SP_BN = 128, SP_BK = 32, SP_THREADS = 256;
+
+__device__ __forceinline__ void decode4(uint32_t w, float *out)
+{
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
+    out[0] = fa.x; out[1] = fa.y; out[2] = fb.x; out[3] = fb.y;
+}
+
+// Simple form: 32 x 128 tiles of decoded values on the fp32 units.  Thread
+// (ty, tx) computes rows 4 ty .. + 3, columns 4 tx .. + 3; a warp holds whole
+// rows of the tile, which is one block of h in the SwiGLU form.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(SP_THREADS) product_simple_kernel(const ProductArgs a)
+{
+    __shared__ float xs[SP_BK][SP_BM + 1];
+    __shared__ float ws[SP_BK][SP_BN + 4];
+    sqd::pdl_launch_dependents();
+    sqd::pdl_wait();
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    // row tile blockIdx.y -> (expert, first row)
+    int64_t lo = 0, hi = a.M;
+    int g = 0;
+    int64_t left = blockIdx.y;
+    for (; g < a.G; ++g) {
+        expert_rows(a, g, lo, hi);
+        const int64_t n = (hi - lo + SP_BM - 1) / SP_BM;
+        if (left < n) break;
+        left -= n;
+    }
+    if (g == a.G) return;
+    const int64_t m0 = lo + left * SP_BM;
+    const int n0 = blockIdx.x * SP_BN;
+    constexpr int MATS = SWIGLU ? 2 : 1;
+    float acc[MATS][4][4] = {};
+#pragma unroll
+    for (int mat = 0; mat < MATS; ++mat) {
+        const int64_t wg = static_cast<int64_t>(g) * MATS + mat;
+        for (int b = 0; b < a.kb; ++b) {
+            float part[4][4] = {};
+            for (int kk = 0; kk < BLK; kk += SP_BK) {
+                __syncthreads();
+                {
+                    const int r = threadIdx.x >> 3, q = (threadIdx.x & 7) * 4;
+                    float f[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (m0 + r < hi) decode4(*reinterpret_cast<const uint32_t *>(a.X_8 + (m0 + r) * a.k_pad + b * BLK + kk + q), f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) xs[q + i][r] = f[i];
+                }
+                {
+                    const int r = threadIdx.x >> 1, q = (threadIdx.x & 1) * 16;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (n0 + r < a.N) v = *reinterpret_cast<const uint4 *>(a.W_8 + (wg * a.N + n0 + r) * a.k_pad + b * BLK + kk + q);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        float f[4];
+                        decode4(w[p], f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ws[q + 4 * p + i][r] = f[i];
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < SP_BK; ++k) {
+                    float xv[4], wv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) xv[i] = xs[k][4 * ty + i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) wv[j] = ws[k][4 * tx + j];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xv[i], wv[j], part[i][j]);
+                }
+            }
+            const float sw = a.s_w[(wg * a.nb + blockIdx.x) * a.s_ld + b];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t m = m0 + 4 * ty + i;
+                const float s = m < hi ? a.s_x[m * a.s_ld + b] * sw : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[mat][i][j] = fmaf(part[i][j], s, acc[mat][i][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + 4 * ty + i;
+        const int n = n0 + 4 * tx;
+        if constexpr (SWIGLU) {
+            float h[4], mx = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = n + j < a.N ? silu_mul(acc[0][i][j], acc[MATS - 1][i][j]) : 0.0f;
+                mx = fmaxf(mx, fabsf(h[j]));
+            }
+            mx = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)));
+            const float s = __fdiv_rn(mx, kTop);
+            if (m < hi) {
+                uint32_t c = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    c |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(s > 0.0f ? __fdiv_rn(h[j], s) : 0.0f, __NV_SATFINITE, __NV_E4M3)) << (8 * j);
+                *reinterpret_cast<uint32_t *>(a.H_8 + m * a.h_pad + n) = c;
+                if (tx == 0) a.s_h[m * a.h_ld + blockIdx.x] = s;
+                // the zero scales past the last block
+                if (blockIdx.x == gridDim.x - 1 && tx > 0 && static_cast<int>(blockIdx.x) + tx < a.h_ld)
+                    a.s_h[m * a.h_ld + blockIdx.x + tx] = 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (m < hi && n + j < a.N) a.Y[m * a.ldy + n + j] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][i][j]));
+        }
+    }
+}
+
+}  // namespace sqb
