@@ -19,6 +19,7 @@
 #include "../../include/sq.h"
 #include "sq_device.cuh"
 #include "sq_fp8b.cuh"
+#include "sq_fp8b_pair.cuh"
 #include "sq_gemm_common.cuh"
 #include "sq_gemm_pair.cuh"
 #include "sq_gemm_skinny.cuh"

@@ -99,11 +99,41 @@ sq_status quant_fp8b_impl(const void *X, int64_t M, int64_t K, int64_t ldx, cons
 }
 
 // ---------------------------------------------------------------- products
+// 256 x 256 tiles (SwiGLU: 256 x 128 of h) on CTA pairs.
+template <bool SWIGLU>
+sq_status launch_pair(const DevInfo &di, const sqb::ProductArgs &a, cudaStream_t stream)
+{
+    constexpr int MATS = SWIGLU ? 2 : 1;
+    const int64_t w_rows = static_cast<int64_t>(a.G) * MATS * a.N;
+    if (w_rows > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld weight rows", (long long)w_rows);
+    CUtensorMap m_x{}, m_w{}, m_y{};
+    SQ_TRY(make_map(m_x, a.X_8, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k_pad, a.M, a.k_pad, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B));
+    SQ_TRY(make_map(m_w, a.W_8, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k_pad, w_rows, a.k_pad, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B));
+    if (!SWIGLU)
+        SQ_TRY(make_map(m_y, a.Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.N, a.M, static_cast<uint64_t>(a.ldy) * 2, 64, 32,
+                        CU_TENSOR_MAP_SWIZZLE_128B));
+    sqb::PairArgs pa;
+    pa.p = a;
+    pa.nt = SWIGLU ? a.nb : (a.nb + 1) / 2;
+    const int64_t mt = (a.M + sqb::PP_BM - 1) / sqb::PP_BM;
+    pa.group_m = raster_group(static_cast<int>(mt), sqb::PP_BM, 2 * a.k_pad, 0);
+    const int64_t tiles = (mt + (a.offsets ? std::min<int64_t>(a.G, a.M) : 0)) * pa.nt;
+    const int64_t clusters = std::min<int64_t>(tiles, di.sms / 2);
+    const size_t smem = sqb::pp_smem_bytes(a.G);
+    auto kern = sqb::product_pair_kernel<SWIGLU>;
+    int per_sm = 0;
+    SQ_TRY(kernel_setup(reinterpret_cast<const void *>(kern), sqb::PP_THREADS, smem, per_sm, "block-scaled pair set-up"));
+    const cudaError_t e = launch_k(kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(sqb::PP_THREADS), smem, stream, 0u, m_x,
+                                   m_w, m_y, pa);
+    return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled pair launch");
+}
+
 template <bool SWIGLU>
 sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
 {
     DevInfo di;
     SQ_TRY(device_info(di));
+    if (a.M > (a.offsets ? 128ll * a.G : 128ll)) return launch_pair<SWIGLU>(di, a, stream);
     const int64_t tiles_m = (a.M + sqb::SP_BM - 1) / sqb::SP_BM + (a.offsets ? std::min<int64_t>(a.G, a.M) : 0);
     if (tiles_m > 65535) return fail(SQ_ERR_UNSUPPORTED, "M=%lld rows", (long long)a.M);
     const cudaError_t e = launch_k(sqb::product_simple_kernel<SWIGLU>, dim3(static_cast<unsigned>(a.nb), static_cast<unsigned>(tiles_m)),

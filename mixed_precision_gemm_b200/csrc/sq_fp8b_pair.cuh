@@ -1,0 +1,408 @@
+// Block-scaled FP8 products on CTA pairs (many rows): tcgen05 kind::f8f6f4 with
+// every 128-channel block of sums scaled on its way out of tensor memory.
+//
+//   Y[m,n] = sum_b sx[m,b] sw[n/128,b] * D_b[m,n],   D_b = E4M3 products of block b
+//
+// The scales differ from block to block, so D_b cannot stay in one accumulator.
+// A 256 x 256 tile's blocks alternate between two TMEM buffers of 256 columns:
+// while the tensor cores fill one (4 MMAs of 32 channels), the eight epilogue
+// warps of each CTA read the other and add it, times its scale, to the tile's
+// sums, which live in their registers (a warp: 32 rows x 128 columns, 128 fp32
+// registers a thread; a thread's row and half tile share one scale per block).
+// Per block a CTA reads 128 KB from TMEM beside 512 cycles of MMA.
+//
+// Warps of each CTA: 0 loads (TMA, a ring of 128-channel blocks: 128 rows of X
+// and 128 rows of W per CTA), 1 issues the pair's MMAs (first CTA), 2 and 3 only
+// give their registers away, 4..11 epilogue (TMEM lane quarter w % 4, column half
+// (w - 4) / 4).
+// Persistent over the tiles of all experts; the rows of X and Y are the
+// experts' rows one after the other, an expert's last tile is cut by rows when
+// it is stored.
+//
+// SwiGLU form: the pair's first CTA loads gate rows and the second one up rows of
+// the same 128 columns, so that a tile's halves are x G^T and x U^T of one
+// 128-column block of h.  The two warps of a lane quarter exchange half of their
+// sums through shared memory, each forms 64 columns of h = silu(g) u, and with
+// the block's largest magnitude (both warps' maxima) writes their E4M3 codes: h
+// never leaves the SM in another form.
+#pragma once
+
+#include "sq_fp8b.cuh"
+#include "sq_gemm_common.cuh"
+
+namespace sqb {
+
+constexpr int PP_BM = 256, PP_BN = 256;
+constexpr int PP_EPI0 = 4, PP_EPI = 8;
+constexpr int PP_REGS_IO = 56, PP_REGS_EPI = 224;  // of the 168 a thread that 12 warps are launched with: 4 * 56 + 8 * 224 = 12 * 168
+constexpr int PP_THREADS = 32 * (PP_EPI0 + PP_EPI);
+constexpr int PP_OPS = 5;                        // ring stages
+constexpr int PP_STAGE = 256 * 128;              // bytes per CTA: 128 rows of X, 128 of W
+constexpr int PP_OFF_BOX = PP_OPS * PP_STAGE;    // per epilogue warp 8 KB: two 32 x 64 bf16 boxes, or 16 x 512 B of sums
+constexpr int PP_OFF_BAR = PP_OFF_BOX + PP_EPI * 8192;
+constexpr int PP_NBAR = 2 * PP_OPS + 9;          // full[OPS] empty[OPS] acc_full[2] acc_empty[2] drain swap[4]
+constexpr int PP_OFF_MISC = PP_OFF_BAR + 8 * PP_NBAR;   // TMEM address, abort flag
+constexpr int PP_OFF_OFFS = PP_OFF_MISC + 8;     // row offsets of the experts
+constexpr int pp_smem_bytes(int G) { return PP_OFF_OFFS + 4 * (G + 1) + 768; }
+static_assert(pp_smem_bytes(512) <= 232448, "shared memory");
+static_assert(PP_OFF_BOX % 1024 == 0, "swizzled boxes");
+
+enum : unsigned { SITE_PP_LOAD = 0x601, SITE_PP_MMA = 0x602, SITE_PP_ACC = 0x603, SITE_PP_EPI = 0x604 };
+
+// Tiles of all experts in order: inside an expert, bands of group_m row tiles
+// sweep the column tiles, so that a W tile is fetched for a whole band.
+struct TileWalk {
+    const int32_t *off;
+    int G, nt, group_m;
+    int e, base, cnt, mt;
+
+    __device__ TileWalk(const int32_t *off_, int G_, int nt_, int group_m_)
+        : off(off_), G(G_), nt(nt_), group_m(group_m_), e(-1), base(0), cnt(0), mt(0) {}
+
+    // The expert of tile t (calls with growing t); false behind the last one.
+    __device__ bool seek(int t)
+    {
+        while (t >= base + cnt) {
+            base += cnt;
+            if (++e >= G) {
+                cnt = 0;
+                e = G;
+                return false;
+            }
+            mt = max(0, (off[e + 1] - off[e] + PP_BM - 1) / PP_BM);
+            cnt = mt * nt;
+        }
+        return true;
+    }
+    __device__ void coords(int t, int &tmi, int &tni) const
+    {
+        const int idx = t - base;
+        const int gsz = group_m * nt;
+        const int g = idx / gsz;
+        const int gm = min(mt - g * group_m, group_m);
+        const int r = idx - g * gsz;
+        tmi = g * group_m + r % gm;
+        tni = r / gm;
+    }
+};
+
+struct PairArgs {
+    ProductArgs p;
+    int nt, group_m;
+};
+
+template <bool SWIGLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PP_THREADS, 1)
+product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_y, const PairArgs args)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];   // (the round-up covers a base that is only 256-byte aligned)
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = sqd::smem_u32(smem);
+    const ProductArgs &p = args.p;
+    constexpr int MATS = SWIGLU ? 2 : 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = sqd::cluster_ctarank();
+    sqd::pdl_launch_dependents();
+
+    const uint32_t bar0 = sbase + PP_OFF_BAR;
+    auto full = [&](int e) { return bar0 + 8u * e; };
+    auto empty = [&](int e) { return bar0 + 8u * (PP_OPS + e); };
+    auto acc_full = [&](int r) { return bar0 + 8u * (2 * PP_OPS + r); };
+    auto acc_empty = [&](int r) { return bar0 + 8u * (2 * PP_OPS + 2 + r); };
+    const uint32_t drain = bar0 + 8u * (2 * PP_OPS + 4);
+    auto swap = [&](int q) { return bar0 + 8u * (2 * PP_OPS + 5 + q); };   // SwiGLU: the two warps of lane quarter q
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PP_OFF_MISC);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + PP_OFF_MISC + 4);
+    int32_t *offs = reinterpret_cast<int32_t *>(smem + PP_OFF_OFFS);
+    auto stage = [&](int e) { return sbase + e * PP_STAGE; };
+
+    if (threadIdx.x == 0) {
+        for (int e = 0; e < PP_OPS; ++e) {
+            sqd::mbar_init(full(e), 2);    // each CTA's loading thread, with its bytes (first CTA's copy)
+            sqd::mbar_init(empty(e), 1);   // multicast commit
+        }
+        for (int r = 0; r < 2; ++r) {
+            sqd::mbar_init(acc_full(r), 1);              // multicast commit
+            sqd::mbar_init(acc_empty(r), 2 * PP_EPI);    // both CTAs' epilogue warps (first CTA's copy)
+        }
+        sqd::mbar_init(drain, 1);
+        for (int q = 0; q < 4; ++q) sqd::mbar_init(swap(q), 2);
+        *abort_flag = 0u;
+        sqd::fence_barrier_init();
+        sqd::fence_proxy_async_smem();
+        sqd::prefetch_tensormap(&tm_x);
+        sqd::prefetch_tensormap(&tm_w);
+        if (!SWIGLU) sqd::prefetch_tensormap(&tm_y);
+    }
+    if (warp == 1) {
+        sqd::tmem_alloc_pair(sqd::smem_u32(tmem_slot), 512);
+        sqd::tmem_relinquish_pair();
+    }
+    sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
+    for (int g = threadIdx.x; g <= p.G; g += PP_THREADS) {
+        // growing and inside the rows, whatever the offsets hold
+        int64_t o = p.offsets ? p.offsets[g] : (g ? p.M : 0);
+        offs[g] = static_cast<int32_t>(min(max(o, int64_t(0)), p.M));
+    }
+    sqd::tc_fence_before();
+    sqd::cluster_sync();
+    sqd::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int kb = p.kb;
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    TileWalk walk(offs, p.G, args.nt, args.group_m);
+
+    if (warp < PP_EPI0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PP_REGS_IO));
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            int e = 0, last = -1;
+            uint32_t ph = 0, last_ph = 0;
+            bool ok = true;
+            for (int t = pair; ok && walk.seek(t); t += pairs) {
+                int tmi, tni;
+                walk.coords(t, tmi, tni);
+                const int xr = offs[walk.e] + tmi * PP_BM + static_cast<int>(rank) * 128;
+                const int wr = SWIGLU ? (walk.e * 2 + static_cast<int>(rank)) * p.N + tni * 128
+                                      : walk.e * p.N + tni * PP_BN + static_cast<int>(rank) * 128;
+                for (int b = 0; b < kb; ++b) {
+                    if (!sqd::mbar_wait(empty(e), ph ^ 1u, abort_flag, SITE_PP_LOAD)) { ok = false; break; }
+                    const uint32_t bar = sqd::map_to_cta(full(e), 0);
+                    sqd::mbar_arrive_expect_tx_cluster(bar, PP_STAGE);
+                    sqd::tma_load_2d_pair(stage(e), &tm_x, bar, b * BLK, xr);
+                    sqd::tma_load_2d_pair(stage(e) + 128 * 128, &tm_w, bar, b * BLK, wr);
+                    last = e;
+                    last_ph = ph;
+                    if (++e == PP_OPS) { e = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok && last >= 0 && rank == 0) sqd::mbar_drain(full(last), last_ph);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs (first CTA)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc = sqd::make_idesc_e4m3(PP_BM, PP_BN);
+            int e = 0;
+            uint32_t ph = 0, g = 0;
+            bool ok = true;
+            for (int t = pair; ok && walk.seek(t); t += pairs) {
+                for (int b = 0; b < kb; ++b, ++g) {
+                    const uint32_t r = g & 1u;
+                    if (!sqd::mbar_wait(acc_empty(r), ((g >> 1) & 1u) ^ 1u, abort_flag, SITE_PP_ACC) ||
+                        !sqd::mbar_wait(full(e), ph, abort_flag, SITE_PP_MMA)) { ok = false; break; }
+                    sqd::tc_fence_after();
+                    const uint64_t ad = sqd::make_sw128_desc(stage(e));
+                    const uint64_t bd = sqd::make_sw128_desc(stage(e) + 128 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sqd::mma_f8_pair(tmem + r * PP_BN, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                    sqd::mma_commit_pair_multicast(empty(e), 0x3);
+                    sqd::mma_commit_pair_multicast(acc_full(r), 0x3);
+                    if (++e == PP_OPS) { e = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok) {
+                sqd::mma_commit_pair(drain);
+                sqd::mbar_drain(drain, 0);
+            }
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PP_REGS_EPI));
+        // ------------------------------------------------------------ sums and stores
+        const int quarter = warp & 3, half = (warp - PP_EPI0) >> 2;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+        const uint32_t empty0[2] = {sqd::map_to_cta(acc_empty(0), 0), sqd::map_to_cta(acc_empty(1), 0)};
+        const uint32_t box = sbase + PP_OFF_BOX + (warp - PP_EPI0) * 8192;
+        const uint32_t partner = sbase + PP_OFF_BOX + ((warp - PP_EPI0) ^ 4) * 8192;
+        const int srow = static_cast<int>(rank) * 128 + quarter * 32;   // the warp's first row of the tile
+        uint32_t g = 0;
+        int t = pair;
+        bool more = walk.seek(t), ok = true;
+
+        // where the current tile lies, and its scales of four blocks
+        int e_now = 0, tmi = 0, tni = 0, row0 = 0, row_end = 0;
+        const float4 *sx_p = nullptr, *sw_p = nullptr;
+        float4 sx4 = make_float4(0.f, 0.f, 0.f, 0.f), sw4 = sx4;
+        auto open_tile = [&]() {
+            walk.coords(t, tmi, tni);
+            e_now = walk.e;
+            row0 = offs[e_now] + tmi * PP_BM + srow;
+            row_end = offs[e_now + 1];
+            const int blk = SWIGLU ? tni : tni * 2 + half;
+            const bool row_ok = row0 + lane < row_end, col_ok = blk < p.nb;
+            sx_p = row_ok ? reinterpret_cast<const float4 *>(p.s_x + static_cast<int64_t>(row0 + lane) * p.s_ld) : nullptr;
+            sw_p = col_ok ? reinterpret_cast<const float4 *>(
+                                p.s_w + (static_cast<int64_t>(e_now * MATS + (SWIGLU ? half : 0)) * p.nb + blk) * p.s_ld)
+                          : nullptr;
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            sx4 = sx_p ? __ldg(sx_p) : z;
+            sw4 = sw_p ? __ldg(sw_p) : z;
+        };
+        // both warps of the lane quarter have come here, and see what the other has stored
+        uint32_t met = 0;
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) sqd::mbar_arrive(swap(quarter));
+            const bool there = sqd::mbar_wait(swap(quarter), met, abort_flag, SITE_PP_EPI);
+            met ^= 1u;
+            return there;
+        };
+        if (more) open_tile();
+        while (more) {
+            uint64_t acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+            for (int b0 = 0; b0 < kb && ok; b0 += 4) {
+                const float sc[4] = {sx4.x * sw4.x, sx4.y * sw4.y, sx4.z * sw4.z, sx4.w * sw4.w};
+                if (b0 + 4 < kb) {
+                    if (sx_p) sx4 = __ldg(sx_p + (b0 >> 2) + 1);
+                    if (sw_p) sw4 = __ldg(sw_p + (b0 >> 2) + 1);
+                }
+                const int nb4 = min(4, kb - b0);
+#pragma unroll 1
+                for (int q = 0; q < nb4; ++q, ++g) {
+                    const float s = q == 0 ? sc[0] : q == 1 ? sc[1] : q == 2 ? sc[2] : sc[3];
+                    const uint64_t s2 = sqq::f2_pack(__float_as_uint(s), __float_as_uint(s));
+                    const uint32_t r = g & 1u;
+                    if (!sqd::mbar_wait(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI)) { ok = false; break; }
+                    sqd::tc_fence_after();
+                    const uint32_t src = tl + r * PP_BN;
+                    uint32_t v[2][16];
+                    sqd::tmem_ld_32x32b_x16(src, v[0]);
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        sqd::tmem_wait_ld_dep1(v[ch & 1]);
+                        if (ch < 7) sqd::tmem_ld_32x32b_x16(src + 16 * (ch + 1), v[(ch + 1) & 1]);
+                        else {
+                            // everything read: the buffer goes back to the MMAs
+                            sqd::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) sqd::mbar_arrive_cluster(empty0[r]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[8 * ch + i] = sqq::f2_fma(sqq::f2_pack(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), s2, acc[8 * ch + i]);
+                    }
+                }
+            }
+            if (!ok) break;
+            // the tile's place, before the next one's scales are fetched
+            const int c_row0 = row0, c_end = row_end, c_tni = tni;
+            t += pairs;
+            more = walk.seek(t);
+            if (more) open_tile();
+
+            if constexpr (SWIGLU) {
+                // gate warps hand over columns 64.., up warps columns ..63; then column c of
+                // this warp (half 0: c < 64, half 1: c >= 64) has both sums here
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t a, b2, c, d;
+                    // (selects, not an indexed array: acc has to stay in registers)
+                    sqq::f2_unpack(half ? acc[2 * i] : acc[32 + 2 * i], a, b2);
+                    sqq::f2_unpack(half ? acc[2 * i + 1] : acc[32 + 2 * i + 1], c, d);
+                    sqd::sts128(partner + i * 512 + lane * 16, a, b2, c, d);
+                }
+                if (!meet()) break;
+                float h[64];
+                float mx = 0.0f;
+                const int n0 = c_tni * 128 + half * 64;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t own[4];
+                    sqq::f2_unpack(half ? acc[32 + 2 * i] : acc[2 * i], own[0], own[1]);
+                    sqq::f2_unpack(half ? acc[32 + 2 * i + 1] : acc[2 * i + 1], own[2], own[3]);
+                    const uint4 o = sqd::lds128(box + i * 512 + lane * 16);
+                    const uint32_t oth[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float gt = __uint_as_float(half ? oth[j] : own[j]), upv = __uint_as_float(half ? own[j] : oth[j]);
+                        const float hv = n0 + 4 * i + j < p.N ? silu_mul(gt, upv) : 0.0f;
+                        h[4 * i + j] = hv;
+                        mx = fmaxf(mx, fabsf(hv));
+                    }
+                }
+                __syncwarp();   // this warp has read its box: the maxima go there
+                sqd::sts32(box + 4 * lane, __float_as_uint(mx));
+                if (!meet()) break;
+                mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
+                const float s = __fdiv_rn(mx, kTop);
+                const int64_t m = c_row0 + lane;
+                if (m < c_end) {
+                    uint8_t *out = p.H_8 + m * p.h_pad + n0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = 0;
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const float2 f = s > 0.0f ? make_float2(__fdiv_rn(h[16 * i + 4 * j + 2 * q], s), __fdiv_rn(h[16 * i + 4 * j + 2 * q + 1], s))
+                                                          : make_float2(0.0f, 0.0f);
+                                w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * q);
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (half == 0) {
+                        p.s_h[m * p.h_ld + c_tni] = s;
+                        if (c_tni == p.nb - 1)
+                            for (int z = p.nb; z < p.h_ld; ++z) p.s_h[m * p.h_ld + z] = 0.0f;
+                    }
+                }
+            } else {
+                const int n0 = c_tni * PP_BN + half * 128;
+                // the previous tile's bulk stores have read the boxes
+                if (lane == 0) sqd::bulk_wait_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a, b2;
+                        sqq::f2_unpack(acc[4 * i + j], a, b2);
+                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b2));
+                        w[j] = *reinterpret_cast<const uint32_t *>(&y2);
+                    }
+                    sqd::sts128(box + (i >> 3) * 4096 + lane * 128 + (((i & 7) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                }
+                if (c_row0 + 32 <= c_end) {
+                    sqd::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (n0 < p.N) sqd::tma_store_2d(&tm_y, box, n0, c_row0);
+                        if (n0 + 64 < p.N) sqd::tma_store_2d(&tm_y, box + 4096, n0 + 64, c_row0);
+                        sqd::bulk_commit();
+                    }
+                } else {
+                    // the expert ends inside these 32 rows: 4 rows x 128 bytes at a time
+                    __syncwarp();
+                    for (int i = 0; i < 16; ++i) {
+                        const int rr = (i & 7) * 4 + (lane >> 3), c = lane & 7;
+                        const int n = n0 + (i >> 3) * 64 + c * 8;
+                        const uint4 v = sqd::lds128(box + (i >> 3) * 4096 + rr * 128 + ((c ^ (rr & 7)) << 4));
+                        if (c_row0 + rr < c_end && n < p.N)
+                            *reinterpret_cast<uint4 *>(p.Y + static_cast<int64_t>(c_row0 + rr) * p.ldy + n) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!SWIGLU && lane == 0) sqd::bulk_wait_all();
+    }
+
+    __syncwarp();
+    sqd::tc_fence_before();
+    sqd::cluster_sync();  // every MMA and every TMEM read of both CTAs is done
+    if (warp == 1) {
+        sqd::tc_fence_after();
+        sqd::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+}  // namespace sqb
