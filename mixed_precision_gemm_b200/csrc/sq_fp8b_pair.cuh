@@ -5,26 +5,28 @@
 //
 // The scales differ from block to block, so D_b cannot stay in one accumulator.
 // A 256 x 256 tile's blocks alternate between two TMEM buffers of 256 columns:
-// while the tensor cores fill one (4 MMAs of 32 channels), the eight epilogue
+// while the tensor cores fill one (4 MMAs of 32 channels), the sixteen epilogue
 // warps of each CTA read the other and add it, times its scale, to the tile's
-// sums, which live in their registers (a warp: 32 rows x 128 columns, 128 fp32
-// registers a thread; a thread's row and half tile share one scale per block).
-// Per block a CTA reads 128 KB from TMEM beside 512 cycles of MMA.
+// sums, which live in their registers (a warp: 32 rows x 64 columns, 64 fp32
+// registers a thread; a thread's row and columns share one scale per block).
+// Per block a CTA reads 128 KB from TMEM beside 512 cycles of MMA; four warps on
+// each scheduler cover the loads' latency (eight warps with 128 sums a thread took
+// 570 cycles from a block's completion to the buffer's release).
 //
 // Warps of each CTA: 0 loads (TMA, a ring of 128-channel blocks: 128 rows of X
 // and 128 rows of W per CTA), 1 issues the pair's MMAs (first CTA), 2 and 3 only
-// give their registers away, 4..11 epilogue (TMEM lane quarter w % 4, column half
-// (w - 4) / 4).
+// give their registers away, 4..19 epilogue (TMEM lane quarter w % 4, 64-column
+// run (w - 4) / 4).
 // Persistent over the tiles of all experts; the rows of X and Y are the
 // experts' rows one after the other, an expert's last tile is cut by rows when
 // it is stored.
 //
 // SwiGLU form: the pair's first CTA loads gate rows and the second one up rows of
 // the same 128 columns, so that a tile's halves are x G^T and x U^T of one
-// 128-column block of h.  The two warps of a lane quarter exchange half of their
-// sums through shared memory, each forms 64 columns of h = silu(g) u, and with
-// the block's largest magnitude (both warps' maxima) writes their E4M3 codes: h
-// never leaves the SM in another form.
+// 128-column block of h.  A gate and an up warp exchange half of their sums through
+// shared memory, each forms 32 columns of h = silu(g) u, and with the block's
+// largest magnitude (the maxima of the lane quarter's four warps) writes their E4M3
+// codes: h never leaves the SM in another form.
 #pragma once
 
 #include "sq_fp8b.cuh"
@@ -34,13 +36,15 @@ namespace sqb {
 
 constexpr int PP_BM = 256, PP_BN = 256;
 constexpr int PP_EPI0 = 4, PP_EPI = 8;
+constexpr int PP_COLS = 128;                       // tile columns per epilogue warp
 constexpr int PP_REGS_IO = 56, PP_REGS_EPI = 224;  // of the 168 a thread that 12 warps are launched with: 4 * 56 + 8 * 224 = 12 * 168
 constexpr int PP_THREADS = 32 * (PP_EPI0 + PP_EPI);
 constexpr int PP_OPS = 5;                        // ring stages
 constexpr int PP_STAGE = 256 * 128;              // bytes per CTA: 128 rows of X, 128 of W
 constexpr int PP_OFF_BOX = PP_OPS * PP_STAGE;    // per epilogue warp 8 KB: two 32 x 64 bf16 boxes, or 16 x 512 B of sums
-constexpr int PP_OFF_BAR = PP_OFF_BOX + PP_EPI * 8192;
-constexpr int PP_NBAR = 2 * PP_OPS + 9;          // full[OPS] empty[OPS] acc_full[2] acc_empty[2] drain swap[4]
+constexpr int PP_BOX = 8192;
+constexpr int PP_OFF_BAR = PP_OFF_BOX + PP_EPI * PP_BOX;
+constexpr int PP_NBAR = 2 * PP_OPS + 10;         // full[OPS] empty[OPS] acc_full[2] acc_empty[2] drain[2] swap[4]
 constexpr int PP_OFF_MISC = PP_OFF_BAR + 8 * PP_NBAR;   // TMEM address, abort flag
 constexpr int PP_OFF_OFFS = PP_OFF_MISC + 8;     // row offsets of the experts
 constexpr int pp_smem_bytes(int G) { return PP_OFF_OFFS + 4 * (G + 1) + 768; }
@@ -110,8 +114,8 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     auto empty = [&](int e) { return bar0 + 8u * (PP_OPS + e); };
     auto acc_full = [&](int r) { return bar0 + 8u * (2 * PP_OPS + r); };
     auto acc_empty = [&](int r) { return bar0 + 8u * (2 * PP_OPS + 2 + r); };
-    const uint32_t drain = bar0 + 8u * (2 * PP_OPS + 4);
-    auto swap = [&](int q) { return bar0 + 8u * (2 * PP_OPS + 5 + q); };   // SwiGLU: the two warps of lane quarter q
+    auto drain = [&](uint32_t r) { return bar0 + 8u * (2 * PP_OPS + 4 + r); };
+    auto swap = [&](int q) { return bar0 + 8u * (2 * PP_OPS + 6 + q); };   // SwiGLU: the two warps of lane quarter q
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PP_OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + PP_OFF_MISC + 4);
     int32_t *offs = reinterpret_cast<int32_t *>(smem + PP_OFF_OFFS);
@@ -124,10 +128,10 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         }
         for (int r = 0; r < 2; ++r) {
             sqd::mbar_init(acc_full(r), 1);              // multicast commit
+            sqd::mbar_init(drain(r), 1);
             sqd::mbar_init(acc_empty(r), 2 * PP_EPI);    // both CTAs' epilogue warps (first CTA's copy)
         }
-        sqd::mbar_init(drain, 1);
-        for (int q = 0; q < 4; ++q) sqd::mbar_init(swap(q), 2);
+        for (int q = 0; q < 4; ++q) sqd::mbar_init(swap(q), PP_EPI / 4);
         *abort_flag = 0u;
         sqd::fence_barrier_init();
         sqd::fence_proxy_async_smem();
@@ -180,43 +184,46 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
             }
             if (!ok && last >= 0 && rank == 0) sqd::mbar_drain(full(last), last_ph);
         }
-    } else if (warp == 1) {
+    } else if (warp < 3) {
         // ------------------------------------------------------------ MMAs (first CTA)
+        // Warp 1 issues the even blocks, warp 2 the odd ones, each into its own TMEM buffer.
         if (rank == 0 && lane == 0) {
             constexpr uint32_t idesc = sqd::make_idesc_e4m3(PP_BM, PP_BN);
-            int e = 0;
-            uint32_t ph = 0, g = 0;
+            const uint64_t desc0 = sqd::make_sw128_desc(stage(0));   // (the ring ends below the address field's 256 KB)
+            const uint32_t r = static_cast<uint32_t>(warp - 1), d = tmem + r * PP_BN;
+            int e = 0;                     // ring stage, its phase and this buffer's
+            uint32_t ph = 0, free_ph = 1, g = 0;
             bool ok = true;
             for (int t = pair; ok && walk.seek(t); t += pairs) {
                 for (int b = 0; b < kb; ++b, ++g) {
-                    const uint32_t r = g & 1u;
-                    if (!sqd::mbar_wait(acc_empty(r), ((g >> 1) & 1u) ^ 1u, abort_flag, SITE_PP_ACC) ||
-                        !sqd::mbar_wait(full(e), ph, abort_flag, SITE_PP_MMA)) { ok = false; break; }
-                    sqd::tc_fence_after();
-                    const uint64_t ad = sqd::make_sw128_desc(stage(e));
-                    const uint64_t bd = sqd::make_sw128_desc(stage(e) + 128 * 128);
+                    if ((g & 1u) == r) {
+                        const uint64_t ad = desc0 + static_cast<uint64_t>(e * (PP_STAGE >> 4));
+                        const uint64_t bd = ad + (128 * 128 >> 4);
+                        if (!sqd::mbar_wait(full(e), ph, abort_flag, SITE_PP_MMA) ||
+                            !sqd::mbar_wait(acc_empty(r), free_ph, abort_flag, SITE_PP_ACC)) { ok = false; break; }
+                        sqd::tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sqd::mma_f8_pair(tmem + r * PP_BN, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                    sqd::mma_commit_pair_multicast(empty(e), 0x3);
-                    sqd::mma_commit_pair_multicast(acc_full(r), 0x3);
+                        for (int k = 0; k < 4; ++k) sqd::mma_f8_pair(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                        sqd::mma_commit_pair_multicast(acc_full(r), 0x3);
+                        sqd::mma_commit_pair_multicast(empty(e), 0x3);
+                        free_ph ^= 1u;
+                    }
                     if (++e == PP_OPS) { e = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
-                sqd::mma_commit_pair(drain);
-                sqd::mbar_drain(drain, 0);
+                sqd::mma_commit_pair(drain(r));
+                sqd::mbar_drain(drain(r), 0);
             }
         }
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PP_REGS_EPI));
         // ------------------------------------------------------------ sums and stores
-        const int quarter = warp & 3, half = (warp - PP_EPI0) >> 2;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+        const int quarter = warp & 3, half = (warp - PP_EPI0) >> 2;   // column half of the tile
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * PP_COLS);
         const uint32_t empty0[2] = {sqd::map_to_cta(acc_empty(0), 0), sqd::map_to_cta(acc_empty(1), 0)};
-        const uint32_t box = sbase + PP_OFF_BOX + (warp - PP_EPI0) * 8192;
-        const uint32_t partner = sbase + PP_OFF_BOX + ((warp - PP_EPI0) ^ 4) * 8192;
+        const uint32_t box = sbase + PP_OFF_BOX + (warp - PP_EPI0) * PP_BOX;
         const int srow = static_cast<int>(rank) * 128 + quarter * 32;   // the warp's first row of the tile
         uint32_t g = 0;
         int t = pair;
@@ -225,7 +232,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         // where the current tile lies, and its scales of four blocks
         int e_now = 0, tmi = 0, tni = 0, row0 = 0, row_end = 0;
         const float4 *sx_p = nullptr, *sw_p = nullptr;
-        float4 sx4 = make_float4(0.f, 0.f, 0.f, 0.f), sw4 = sx4;
+        float4 sx4 = make_float4(0.f, 0.f, 0.f, 0.f), sw4 = sx4, sc = sx4;
         auto open_tile = [&]() {
             walk.coords(t, tmi, tni);
             e_now = walk.e;
@@ -252,43 +259,53 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         };
         if (more) open_tile();
         while (more) {
-            uint64_t acc[64];
+            uint64_t acc2[PP_COLS / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            for (int b0 = 0; b0 < kb && ok; b0 += 4) {
-                const float sc[4] = {sx4.x * sw4.x, sx4.y * sw4.y, sx4.z * sw4.z, sx4.w * sw4.w};
-                if (b0 + 4 < kb) {
-                    if (sx_p) sx4 = __ldg(sx_p + (b0 >> 2) + 1);
-                    if (sw_p) sw4 = __ldg(sw_p + (b0 >> 2) + 1);
-                }
-                const int nb4 = min(4, kb - b0);
+            for (int i = 0; i < PP_COLS / 2; ++i) acc2[i] = 0ull;
 #pragma unroll 1
-                for (int q = 0; q < nb4; ++q, ++g) {
-                    const float s = q == 0 ? sc[0] : q == 1 ? sc[1] : q == 2 ? sc[2] : sc[3];
-                    const uint64_t s2 = sqq::f2_pack(__float_as_uint(s), __float_as_uint(s));
-                    const uint32_t r = g & 1u;
-                    if (!sqd::mbar_wait(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI)) { ok = false; break; }
-                    sqd::tc_fence_after();
-                    const uint32_t src = tl + r * PP_BN;
-                    uint32_t v[2][16];
-                    sqd::tmem_ld_32x32b_x16(src, v[0]);
-#pragma unroll
-                    for (int ch = 0; ch < 8; ++ch) {
-                        sqd::tmem_wait_ld_dep1(v[ch & 1]);
-                        if (ch < 7) sqd::tmem_ld_32x32b_x16(src + 16 * (ch + 1), v[(ch + 1) & 1]);
-                        else {
-                            // everything read: the buffer goes back to the MMAs
-                            sqd::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) sqd::mbar_arrive_cluster(empty0[r]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[8 * ch + i] = sqq::f2_fma(sqq::f2_pack(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), s2, acc[8 * ch + i]);
+            for (int b = 0; b < kb; ++b, ++g) {
+                if ((b & 3) == 0) {
+                    sc = make_float4(sx4.x * sw4.x, sx4.y * sw4.y, sx4.z * sw4.z, sx4.w * sw4.w);
+                    if (b + 4 < kb) {
+                        if (sx_p) sx4 = __ldg(sx_p + (b >> 2) + 1);
+                        if (sw_p) sw4 = __ldg(sw_p + (b >> 2) + 1);
                     }
+                }
+                const uint64_t s2 = sqq::f2_pack(__float_as_uint(sc.x), __float_as_uint(sc.x));
+                sc = make_float4(sc.y, sc.z, sc.w, 0.0f);
+                const uint32_t r = g & 1u;
+                // (a wait that gave up does not leave the loop: a second way out would cost
+                // copies of all the sums; what is added then is never stored)
+                ok = sqd::mbar_wait(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
+                sqd::tc_fence_after();
+                const uint32_t src = tl + r * PP_BN;
+                uint32_t v[2][16];
+                sqd::tmem_ld_32x32b_x16(src, v[0]);
+#pragma unroll
+                for (int ch = 0; ch < PP_COLS / 16; ++ch) {
+                    sqd::tmem_wait_ld_dep1(v[ch & 1]);
+                    if (ch + 1 < PP_COLS / 16) {
+                        sqd::tmem_ld_32x32b_x16(src + 16 * (ch + 1), v[(ch + 1) & 1]);
+                    } else {
+                        // everything read: the buffer goes back to the MMAs
+                        sqd::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) sqd::mbar_arrive_cluster(empty0[r]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc2[8 * ch + i] = sqq::f2_fma(sqq::f2_pack(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), s2, acc2[8 * ch + i]);
                 }
             }
             if (!ok) break;
+            float acc[PP_COLS];
+#pragma unroll
+            for (int i = 0; i < PP_COLS / 2; ++i) {
+                uint32_t a, b2;
+                sqq::f2_unpack(acc2[i], a, b2);
+                acc[2 * i] = __uint_as_float(a);
+                acc[2 * i + 1] = __uint_as_float(b2);
+            }
             // the tile's place, before the next one's scales are fetched
             const int c_row0 = row0, c_end = row_end, c_tni = tni;
             t += pairs;
@@ -296,36 +313,34 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
             if (more) open_tile();
 
             if constexpr (SWIGLU) {
-                // gate warps hand over columns 64.., up warps columns ..63; then column c of
-                // this warp (half 0: c < 64, half 1: c >= 64) has both sums here
+                // Gate and up warp of the same rows exchange halves: the gate warp hands over its
+                // columns 64.., the up warp its columns ..63; then 64 columns of both are here.
+                const uint32_t partner = sbase + PP_OFF_BOX + ((warp - PP_EPI0) ^ 4) * PP_BOX;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    uint32_t a, b2, c, d;
                     // (selects, not an indexed array: acc has to stay in registers)
-                    sqq::f2_unpack(half ? acc[2 * i] : acc[32 + 2 * i], a, b2);
-                    sqq::f2_unpack(half ? acc[2 * i + 1] : acc[32 + 2 * i + 1], c, d);
-                    sqd::sts128(partner + i * 512 + lane * 16, a, b2, c, d);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(half ? acc[4 * i + j] : acc[64 + 4 * i + j]);
+                    sqd::sts128(partner + i * 512 + lane * 16, o[0], o[1], o[2], o[3]);
                 }
                 if (!meet()) break;
-                float h[64];
                 float mx = 0.0f;
                 const int n0 = c_tni * 128 + half * 64;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    uint32_t own[4];
-                    sqq::f2_unpack(half ? acc[32 + 2 * i] : acc[2 * i], own[0], own[1]);
-                    sqq::f2_unpack(half ? acc[32 + 2 * i + 1] : acc[2 * i + 1], own[2], own[3]);
                     const uint4 o = sqd::lds128(box + i * 512 + lane * 16);
-                    const uint32_t oth[4] = {o.x, o.y, o.z, o.w};
+                    const float oth[4] = {__uint_as_float(o.x), __uint_as_float(o.y), __uint_as_float(o.z), __uint_as_float(o.w)};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float gt = __uint_as_float(half ? oth[j] : own[j]), upv = __uint_as_float(half ? own[j] : oth[j]);
+                        const float own = half ? acc[64 + 4 * i + j] : acc[4 * i + j];
+                        const float gt = half ? oth[j] : own, upv = half ? own : oth[j];
                         const float hv = n0 + 4 * i + j < p.N ? silu_mul(gt, upv) : 0.0f;
-                        h[4 * i + j] = hv;
+                        acc[4 * i + j] = hv;   // (the columns ..63 are used up)
                         mx = fmaxf(mx, fabsf(hv));
                     }
                 }
-                __syncwarp();   // this warp has read its box: the maxima go there
+                __syncwarp();   // this warp has read its box: its rows' maxima go there
                 sqd::sts32(box + 4 * lane, __float_as_uint(mx));
                 if (!meet()) break;
                 mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
@@ -341,7 +356,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                             w[j] = 0;
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                const float2 f = s > 0.0f ? make_float2(__fdiv_rn(h[16 * i + 4 * j + 2 * q], s), __fdiv_rn(h[16 * i + 4 * j + 2 * q + 1], s))
+                                const float2 f = s > 0.0f ? make_float2(__fdiv_rn(acc[16 * i + 4 * j + 2 * q], s), __fdiv_rn(acc[16 * i + 4 * j + 2 * q + 1], s))
                                                           : make_float2(0.0f, 0.0f);
                                 w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * q);
                             }
@@ -355,7 +370,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                     }
                 }
             } else {
-                const int n0 = c_tni * PP_BN + half * 128;
+                const int n0 = c_tni * PP_BN + half * PP_COLS;
                 // the previous tile's bulk stores have read the boxes
                 if (lane == 0) sqd::bulk_wait_read<0>();
                 __syncwarp();
@@ -364,9 +379,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t a, b2;
-                        sqq::f2_unpack(acc[4 * i + j], a, b2);
-                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b2));
+                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(acc[8 * i + 2 * j], acc[8 * i + 2 * j + 1]);
                         w[j] = *reinterpret_cast<const uint32_t *>(&y2);
                     }
                     sqd::sts128(box + (i >> 3) * 4096 + lane * 128 + (((i & 7) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
