@@ -5,28 +5,36 @@
 //
 // The scales differ from block to block, so D_b cannot stay in one accumulator.
 // A 256 x 256 tile's blocks alternate between two TMEM buffers of 256 columns:
-// while the tensor cores fill one (4 MMAs of 32 channels), the sixteen epilogue
+// while the tensor cores fill one (4 MMAs of 32 channels), the eight epilogue
 // warps of each CTA read the other and add it, times its scale, to the tile's
-// sums, which live in their registers (a warp: 32 rows x 64 columns, 64 fp32
-// registers a thread; a thread's row and columns share one scale per block).
-// Per block a CTA reads 128 KB from TMEM beside 512 cycles of MMA; four warps on
-// each scheduler cover the loads' latency (eight warps with 128 sums a thread took
-// 570 cycles from a block's completion to the buffer's release).
+// sums, which live in their registers (a warp: 32 rows x 128 columns, 128 fp32
+// registers a thread; a thread's row and half tile share one scale per block).
+//
+// Measured on a B200 at 4096 x 8192 x 8192, cycles per block of a tile: the MMAs
+// alone 629 (operands in shared memory are read at 96 and written at 64 bytes per
+// 128-cycle MMA and clock, so shared memory bounds them, not the 512 of the
+// tensor pipe); with the sums about 850.  What the sums are made of matters:
+//   - scalar fp32 and integer instructions take cycles from the tensor pipe (4 MMAs
+//     went from 517 to over 800 cycles beside a loop of scalar FMAs), packed ones
+//     (FFMA2) hardly do (587), so the sums are packed and free of register copies;
+//   - one issuing thread's waits and commits left the pipe idle about 460 cycles
+//     per block, so two warps issue alternate blocks;
+//   - sixteen warps of 64 columns were slower (290 us against 252 at this size).
 //
 // Warps of each CTA: 0 loads (TMA, a ring of 128-channel blocks: 128 rows of X
-// and 128 rows of W per CTA), 1 issues the pair's MMAs (first CTA), 2 and 3 only
-// give their registers away, 4..19 epilogue (TMEM lane quarter w % 4, 64-column
-// run (w - 4) / 4).
+// and 128 rows of W per CTA), 1 and 2 issue the pair's MMAs (first CTA), 3 only
+// gives its registers away, 4..11 epilogue (TMEM lane quarter w % 4, column half
+// (w - 4) / 4).
 // Persistent over the tiles of all experts; the rows of X and Y are the
 // experts' rows one after the other, an expert's last tile is cut by rows when
 // it is stored.
 //
 // SwiGLU form: the pair's first CTA loads gate rows and the second one up rows of
 // the same 128 columns, so that a tile's halves are x G^T and x U^T of one
-// 128-column block of h.  A gate and an up warp exchange half of their sums through
-// shared memory, each forms 32 columns of h = silu(g) u, and with the block's
-// largest magnitude (the maxima of the lane quarter's four warps) writes their E4M3
-// codes: h never leaves the SM in another form.
+// 128-column block of h.  The two warps of a lane quarter exchange half of their
+// sums through shared memory, each forms 64 columns of h = silu(g) u, and with
+// the block's largest magnitude (both warps' maxima) writes their E4M3 codes: h
+// never leaves the SM in another form.
 #pragma once
 
 #include "sq_fp8b.cuh"
@@ -37,7 +45,7 @@ namespace sqb {
 constexpr int PP_BM = 256, PP_BN = 256;
 constexpr int PP_EPI0 = 4, PP_EPI = 8;
 constexpr int PP_COLS = 128;                       // tile columns per epilogue warp
-constexpr int PP_REGS_IO = 56, PP_REGS_EPI = 224;  // of the 168 a thread that 12 warps are launched with: 4 * 56 + 8 * 224 = 12 * 168
+constexpr int PP_REGS_IO = 40, PP_REGS_EPI = 232;  // of the 168 a thread that 12 warps are launched with: 4 * 40 + 8 * 232 = 12 * 168
 constexpr int PP_THREADS = 32 * (PP_EPI0 + PP_EPI);
 constexpr int PP_OPS = 5;                        // ring stages
 constexpr int PP_STAGE = 256 * 128;              // bytes per CTA: 128 rows of X, 128 of W
@@ -259,9 +267,9 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         };
         if (more) open_tile();
         while (more) {
-            uint64_t acc2[PP_COLS / 2];
+            float2 sums[PP_COLS / 2];
 #pragma unroll
-            for (int i = 0; i < PP_COLS / 2; ++i) acc2[i] = 0ull;
+            for (int i = 0; i < PP_COLS / 2; ++i) sums[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
             for (int b = 0; b < kb; ++b, ++g) {
                 if ((b & 3) == 0) {
@@ -271,7 +279,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                         if (sw_p) sw4 = __ldg(sw_p + (b >> 2) + 1);
                     }
                 }
-                const uint64_t s2 = sqq::f2_pack(__float_as_uint(sc.x), __float_as_uint(sc.x));
+                const float2 s2 = make_float2(sc.x, sc.x);
                 sc = make_float4(sc.y, sc.z, sc.w, 0.0f);
                 const uint32_t r = g & 1u;
                 // (a wait that gave up does not leave the loop: a second way out would cost
@@ -279,14 +287,12 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                 ok = sqd::mbar_wait(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
                 sqd::tc_fence_after();
                 const uint32_t src = tl + r * PP_BN;
-                uint32_t v[2][16];
-                sqd::tmem_ld_32x32b_x16(src, v[0]);
 #pragma unroll
                 for (int ch = 0; ch < PP_COLS / 16; ++ch) {
-                    sqd::tmem_wait_ld_dep1(v[ch & 1]);
-                    if (ch + 1 < PP_COLS / 16) {
-                        sqd::tmem_ld_32x32b_x16(src + 16 * (ch + 1), v[(ch + 1) & 1]);
-                    } else {
+                    uint32_t v[16];
+                    sqd::tmem_ld_32x32b_x16(src + 16 * ch, v);
+                    sqd::tmem_wait_ld_dep1(v);
+                    if (ch + 1 == PP_COLS / 16) {
                         // everything read: the buffer goes back to the MMAs
                         sqd::tc_fence_before();
                         __syncwarp();
@@ -294,17 +300,16 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        acc2[8 * ch + i] = sqq::f2_fma(sqq::f2_pack(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), s2, acc2[8 * ch + i]);
+                        sums[8 * ch + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
+                                                      sums[8 * ch + i]);
                 }
             }
             if (!ok) break;
             float acc[PP_COLS];
 #pragma unroll
             for (int i = 0; i < PP_COLS / 2; ++i) {
-                uint32_t a, b2;
-                sqq::f2_unpack(acc2[i], a, b2);
-                acc[2 * i] = __uint_as_float(a);
-                acc[2 * i + 1] = __uint_as_float(b2);
+                acc[2 * i] = sums[i].x;
+                acc[2 * i + 1] = sums[i].y;
             }
             // the tile's place, before the next one's scales are fetched
             const int c_row0 = row0, c_end = row_end, c_tni = tni;
