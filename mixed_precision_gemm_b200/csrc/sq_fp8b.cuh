@@ -185,7 +185,24 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int g, int64_t
     hi = min(max(static_cast<int64_t>(a.offsets[g + 1]), lo), a.M);
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) u with the hardware's exponential and reciprocal (about 2^-21 of the
+// value, far below the 2^-12 that a product's sum is known to): one MUFU each where
+// expf and an exact quotient cost some 30 instructions.  e^-g = inf gives 0.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// E4M3 codes of two fp32 values over a block's scale (rounded quotients as in
+// sq_rowquant.cuh), in the low 16 bits.
+__device__ __forceinline__ uint32_t codes2(float x, float y, const BlockScale &b)
+{
+    if (b.zero) return 0u;
+    uint64_t v = sqq::f2_pack(__float_as_uint(x), __float_as_uint(y));
+    if (b.up) v = sqq::f2_mul(v, b.rs.up2);
+    const uint64_t q0 = sqq::f2_mul(v, b.rs.inv2);
+    const uint64_t q1 = sqq::f2_fma(sqq::f2_fma(q0, b.rs.negs2, v), b.rs.inv2, q0);
+    uint32_t t0, t1;
+    sqq::f2_unpack(q1, t0, t1);
+    return __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(t0), __uint_as_float(t1)), __NV_SATFINITE, __NV_E4M3);
+}
 
 constexpr int SP_BM = 32, SP_BN = 128, SP_BK = 32, SP_THREADS = 256;
 
@@ -286,14 +303,10 @@ __global__ void __launch_bounds__(SP_THREADS) product_simple_kernel(const Produc
                 mx = fmaxf(mx, fabsf(h[j]));
             }
             mx = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)));
-            const float s = __fdiv_rn(mx, kTop);
+            const BlockScale bs = block_scale(mx);
             if (m < hi) {
-                uint32_t c = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(s > 0.0f ? __fdiv_rn(h[j], s) : 0.0f, __NV_SATFINITE, __NV_E4M3)) << (8 * j);
-                *reinterpret_cast<uint32_t *>(a.H_8 + m * a.h_pad + n) = c;
-                if (tx == 0) a.s_h[m * a.h_ld + blockIdx.x] = s;
+                *reinterpret_cast<uint32_t *>(a.H_8 + m * a.h_pad + n) = codes2(h[0], h[1], bs) | (codes2(h[2], h[3], bs) << 16);
+                if (tx == 0) a.s_h[m * a.h_ld + blockIdx.x] = bs.s;
                 // the zero scales past the last block
                 if (blockIdx.x == gridDim.x - 1 && tx > 0 && static_cast<int>(blockIdx.x) + tx < a.h_ld)
                     a.s_h[m * a.h_ld + blockIdx.x + tx] = 0.0f;

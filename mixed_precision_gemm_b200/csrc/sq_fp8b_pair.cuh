@@ -349,7 +349,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                 sqd::sts32(box + 4 * lane, __float_as_uint(mx));
                 if (!meet()) break;
                 mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
-                const float s = __fdiv_rn(mx, kTop);
+                const BlockScale bs = block_scale(mx);
                 const int64_t m = c_row0 + lane;
                 if (m < c_end) {
                     uint8_t *out = p.H_8 + m * p.h_pad + n0;
@@ -358,18 +358,13 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            w[j] = 0;
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const float2 f = s > 0.0f ? make_float2(__fdiv_rn(acc[16 * i + 4 * j + 2 * q], s), __fdiv_rn(acc[16 * i + 4 * j + 2 * q + 1], s))
-                                                          : make_float2(0.0f, 0.0f);
-                                w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * q);
-                            }
+                            const float *h = acc + 16 * i + 4 * j;
+                            w[j] = codes2(h[0], h[1], bs) | (codes2(h[2], h[3], bs) << 16);
                         }
                         *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (half == 0) {
-                        p.s_h[m * p.h_ld + c_tni] = s;
+                        p.s_h[m * p.h_ld + c_tni] = bs.s;
                         if (c_tni == p.nb - 1)
                             for (int z = p.nb; z < p.h_ld; ++z) p.s_h[m * p.h_ld + z] = 0.0f;
                     }
