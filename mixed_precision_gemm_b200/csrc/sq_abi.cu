@@ -20,6 +20,7 @@
 #include "sq_device.cuh"
 #include "sq_fp8b.cuh"
 #include "sq_fp8b_pair.cuh"
+#include "sq_fp8b_skinny.cuh"
 #include "sq_gemm_common.cuh"
 #include "sq_gemm_pair.cuh"
 #include "sq_gemm_skinny.cuh"

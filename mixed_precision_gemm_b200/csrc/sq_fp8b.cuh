@@ -204,119 +204,4 @@ __device__ __forceinline__ uint32_t codes2(float x, float y, const BlockScale &b
     return __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(t0), __uint_as_float(t1)), __NV_SATFINITE, __NV_E4M3);
 }
 
-constexpr int SP_BM = 32, SP_BN = 128, SP_BK = 32, SP_THREADS = 256;
-
-__device__ __forceinline__ void decode4(uint32_t w, float *out)
-{
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-    const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-    out[0] = fa.x; out[1] = fa.y; out[2] = fb.x; out[3] = fb.y;
-}
-
-// Simple form: 32 x 128 tiles of decoded values on the fp32 units.  Thread
-// (ty, tx) computes rows 4 ty .. + 3, columns 4 tx .. + 3; a warp holds whole
-// rows of the tile, which is one block of h in the SwiGLU form.
-template <bool SWIGLU>
-__global__ void __launch_bounds__(SP_THREADS) product_simple_kernel(const ProductArgs a)
-{
-    __shared__ float xs[SP_BK][SP_BM + 1];
-    __shared__ float ws[SP_BK][SP_BN + 4];
-    sqd::pdl_launch_dependents();
-    sqd::pdl_wait();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    // row tile blockIdx.y -> (expert, first row)
-    int64_t lo = 0, hi = a.M;
-    int g = 0;
-    int64_t left = blockIdx.y;
-    for (; g < a.G; ++g) {
-        expert_rows(a, g, lo, hi);
-        const int64_t n = (hi - lo + SP_BM - 1) / SP_BM;
-        if (left < n) break;
-        left -= n;
-    }
-    if (g == a.G) return;
-    const int64_t m0 = lo + left * SP_BM;
-    const int n0 = blockIdx.x * SP_BN;
-    constexpr int MATS = SWIGLU ? 2 : 1;
-    float acc[MATS][4][4] = {};
-#pragma unroll
-    for (int mat = 0; mat < MATS; ++mat) {
-        const int64_t wg = static_cast<int64_t>(g) * MATS + mat;
-        for (int b = 0; b < a.kb; ++b) {
-            float part[4][4] = {};
-            for (int kk = 0; kk < BLK; kk += SP_BK) {
-                __syncthreads();
-                {
-                    const int r = threadIdx.x >> 3, q = (threadIdx.x & 7) * 4;
-                    float f[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (m0 + r < hi) decode4(*reinterpret_cast<const uint32_t *>(a.X_8 + (m0 + r) * a.k_pad + b * BLK + kk + q), f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) xs[q + i][r] = f[i];
-                }
-                {
-                    const int r = threadIdx.x >> 1, q = (threadIdx.x & 1) * 16;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (n0 + r < a.N) v = *reinterpret_cast<const uint4 *>(a.W_8 + (wg * a.N + n0 + r) * a.k_pad + b * BLK + kk + q);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        float f[4];
-                        decode4(w[p], f);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) ws[q + 4 * p + i][r] = f[i];
-                    }
-                }
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < SP_BK; ++k) {
-                    float xv[4], wv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) xv[i] = xs[k][4 * ty + i];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) wv[j] = ws[k][4 * tx + j];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xv[i], wv[j], part[i][j]);
-                }
-            }
-            const float sw = a.s_w[(wg * a.nb + blockIdx.x) * a.s_ld + b];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t m = m0 + 4 * ty + i;
-                const float s = m < hi ? a.s_x[m * a.s_ld + b] * sw : 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[mat][i][j] = fmaf(part[i][j], s, acc[mat][i][j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * ty + i;
-        const int n = n0 + 4 * tx;
-        if constexpr (SWIGLU) {
-            float h[4], mx = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = n + j < a.N ? silu_mul(acc[0][i][j], acc[MATS - 1][i][j]) : 0.0f;
-                mx = fmaxf(mx, fabsf(h[j]));
-            }
-            mx = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)));
-            const BlockScale bs = block_scale(mx);
-            if (m < hi) {
-                *reinterpret_cast<uint32_t *>(a.H_8 + m * a.h_pad + n) = codes2(h[0], h[1], bs) | (codes2(h[2], h[3], bs) << 16);
-                if (tx == 0) a.s_h[m * a.h_ld + blockIdx.x] = bs.s;
-                // the zero scales past the last block
-                if (blockIdx.x == gridDim.x - 1 && tx > 0 && static_cast<int>(blockIdx.x) + tx < a.h_ld)
-                    a.s_h[m * a.h_ld + blockIdx.x + tx] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (m < hi && n + j < a.N) a.Y[m * a.ldy + n + j] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][i][j]));
-        }
-    }
-}
-
 }  // namespace sqb

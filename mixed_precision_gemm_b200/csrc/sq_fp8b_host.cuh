@@ -128,17 +128,46 @@ sq_status launch_pair(const DevInfo &di, const sqb::ProductArgs &a, cudaStream_t
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled pair launch");
 }
 
+// 128 weight rows x MP rows of X, K split over clusters.
+template <class C>
+sq_status launch_skinny_b(const DevInfo &di, const sqb::ProductArgs &a, cudaStream_t stream)
+{
+    const int64_t w_rows = static_cast<int64_t>(a.G) * C::MATS * a.N;
+    if (w_rows > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld weight rows", (long long)w_rows);
+    CUtensorMap m_x{}, m_w{};
+    SQ_TRY(make_map(m_x, a.X_8, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k_pad, a.M, a.k_pad, 128, C::MP, CU_TENSOR_MAP_SWIZZLE_128B));
+    SQ_TRY(make_map(m_w, a.W_8, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k_pad, w_rows, a.k_pad, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B));
+    // Row chunks: at most one partial one per expert that has rows.
+    const int64_t experts = a.offsets ? std::min<int64_t>(a.G, a.M) : 1;
+    const int64_t tiles = (a.offsets ? a.M / C::MP + experts : (a.M + C::MP - 1) / C::MP) * a.nb;
+    // As many splits as fill the SMs' places once, if every expert had one chunk.
+    int64_t S = static_cast<int64_t>(C::PER_SM) * di.sms / std::max<int64_t>(1, experts * a.nb);
+    S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(S, sqb::SB_MAX_SPLITS), a.kb));
+    if (tiles * S > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld tiles", (long long)tiles);
+    sqb::SkinnyBArgs sa;
+    sa.p = a;
+    sa.splits = static_cast<int>(S);
+    auto kern = sqb::product_skinny_kernel<C>;
+    int per_sm = 0;
+    SQ_TRY(kernel_setup(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, C::SMEM, per_sm, "block-scaled skinny set-up"));
+    const cudaError_t e = launch_k(kern, dim3(static_cast<unsigned>(tiles * S)), dim3(sqb::SB_THREADS), C::SMEM, stream,
+                                   static_cast<unsigned>(S), m_x, m_w, sa);
+    return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled skinny launch");
+}
+
 template <bool SWIGLU>
 sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
 {
     DevInfo di;
     SQ_TRY(device_info(di));
-    if (a.M > (a.offsets ? 128ll * a.G : 128ll)) return launch_pair<SWIGLU>(di, a, stream);
-    const int64_t tiles_m = (a.M + sqb::SP_BM - 1) / sqb::SP_BM + (a.offsets ? std::min<int64_t>(a.G, a.M) : 0);
-    if (tiles_m > 65535) return fail(SQ_ERR_UNSUPPORTED, "M=%lld rows", (long long)a.M);
-    const cudaError_t e = launch_k(sqb::product_simple_kernel<SWIGLU>, dim3(static_cast<unsigned>(a.nb), static_cast<unsigned>(tiles_m)),
-                                   dim3(sqb::SP_THREADS), 0, stream, 0u, a);
-    return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled product launch");
+    // Rows per weight matrix, were they spread evenly (their counts are on the device).
+    const int64_t rows = a.offsets ? (a.M + a.G - 1) / a.G : a.M;
+    if (rows > 128) return launch_pair<SWIGLU>(di, a, stream);
+    if (rows <= 16) return launch_skinny_b<sqb::CfgSkinnyB<16, SWIGLU, SWIGLU ? 3 : 6, 2>>(di, a, stream);
+    if (rows <= 32) return launch_skinny_b<sqb::CfgSkinnyB<32, SWIGLU, SWIGLU ? 3 : 5, 2>>(di, a, stream);
+    if constexpr (SWIGLU) return launch_skinny_b<sqb::CfgSkinnyB<64, true, 5, 1>>(di, a, stream);
+    else if (rows <= 64) return launch_skinny_b<sqb::CfgSkinnyB<64, false, 4, 2>>(di, a, stream);
+    else return launch_skinny_b<sqb::CfgSkinnyB<128, false, 3, 2>>(di, a, stream);
 }
 
 sq_status product_args(sqb::ProductArgs &a, const void *X_8, const float *s_x, const int32_t *offsets, int64_t M, const void *W_8,

@@ -293,7 +293,8 @@ def rows_by_expert(counts):
     return off, int(off[-1])
 
 
-COUNTS = [[1], [0, 3, 0], [5, 0, 1, 16, 17, 0, 2], [130, 1, 0, 127], [40] * 9, [300, 12, 256, 0, 1], [700, 600]]
+COUNTS = [[1], [0, 3, 0], [5, 0, 1, 16, 17, 0, 2], [130, 1, 0, 127], [40] * 9, [300, 12, 256, 0, 1], [700, 600],
+          [300, 12, 700, 0, 1], [0, 0, 900, 0, 33], [1] * 33 + [0] * 40 + [64, 65]]
 
 
 @pytest.mark.parametrize("counts", COUNTS)
