@@ -457,12 +457,28 @@ def sq_select_outliers(Xc: torch.Tensor, W: torch.Tensor, nO: int, group: int, O
 
 # Block-scaled FP8: E4M3 codes u8 [rows, sq_k_pad_fp8b(K)], fp32 scales per 128
 # channels [rows, sq_scale_ld_fp8b(K)] (weights: per 128 x 128 block).
-def _block_device(*tensors) -> None:
-    """The calls below launch on the current device: every tensor has to live there."""
+def _block_device(*tensors) -> int:
+    """The calls below launch on the current device (returned): every tensor has to live there."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.numel() and t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """Handle of the stream, of the device's current one for None (without building a Stream object)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _k_pad(K: int) -> int:
+    return (K + 127) // 128 * 128
+
+
+def _s_ld(K: int) -> int:
+    return (K + 511) // 512 * 4
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -474,7 +490,7 @@ def _expect(t: torch.Tensor, name: str, dtype, *shape) -> None:
     """A contiguous tensor of this type and shape."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
 
 
@@ -499,40 +515,42 @@ def sq_prepare_weights_fp8b(W: torch.Tensor, W_8: torch.Tensor, s_w: torch.Tenso
     if W.dtype != torch.bfloat16:
         raise TypeError(f"W: expected {torch.bfloat16}, got {W.dtype}")
     N, K = W.shape[-2:]
-    W3 = W.unsqueeze(0) if W.dim() == 2 else W if W.dim() == 3 else W.flatten(0, -3)
+    W3 = W.unsqueeze(0) if W.dim() == 2 else W if W.dim() == 3 else W.view(-1, N, K)
     if W3.stride(2) != 1:
         raise ValueError("W: expected unit inner stride")
     G = W3.shape[0]
-    _expect(W_8, "W_8", torch.uint8, *W.shape[:-1], sq_k_pad_fp8b(K))
-    _expect(s_w, "s_w", torch.float32, *W.shape[:-2], -(-N // 128), sq_scale_ld_fp8b(K))
-    _block_device(W, W_8, s_w)
-    st = load().sq_prepare_weights_fp8b(_ptr(W3), G, N, K, W3.stride(1), W3.stride(0), _ptr(W_8), _ptr(s_w),
-                                        _stream(stream))
+    _expect(W_8, "W_8", torch.uint8, *W.shape[:-1], _k_pad(K))
+    _expect(s_w, "s_w", torch.float32, *W.shape[:-2], -(-N // 128), _s_ld(K))
+    dev = _block_device(W, W_8, s_w)
+    st = load().sq_prepare_weights_fp8b(W3.data_ptr(), G, N, K, W3.stride(1), W3.stride(0), W_8.data_ptr(),
+                                        s_w.data_ptr(), _raw_stream(stream, dev))
     _raise(st, "sq_prepare_weights_fp8b")
 
 
 def sq_quant_fp8b(X: torch.Tensor, X_8: torch.Tensor, s_x: torch.Tensor, stream=None) -> None:
     _rowmajor(X, "X", torch.bfloat16)
     M, K = X.shape
-    _expect(X_8, "X_8", torch.uint8, M, sq_k_pad_fp8b(K))
-    _expect(s_x, "s_x", torch.float32, M, sq_scale_ld_fp8b(K))
-    _block_device(X, X_8, s_x)
-    _raise(load().sq_quant_fp8b(_ptr(X), M, K, _ld(X), _ptr(X_8), _ptr(s_x), _stream(stream)), "sq_quant_fp8b")
+    _expect(X_8, "X_8", torch.uint8, M, _k_pad(K))
+    _expect(s_x, "s_x", torch.float32, M, _s_ld(K))
+    dev = _block_device(X, X_8, s_x)
+    st = load().sq_quant_fp8b(X.data_ptr(), M, K, _ld(X), X_8.data_ptr(), s_x.data_ptr(), _raw_stream(stream, dev))
+    _raise(st, "sq_quant_fp8b")
 
 
 def _check_codes(c: torch.Tensor, s: torch.Tensor, names, rows, K: int, scale_rows) -> None:
-    _expect(c, names[0], torch.uint8, *rows, sq_k_pad_fp8b(K))
-    _expect(s, names[1], torch.float32, *scale_rows, sq_scale_ld_fp8b(K))
+    _expect(c, names[0], torch.uint8, *rows, _k_pad(K))
+    _expect(s, names[1], torch.float32, *scale_rows, _s_ld(K))
 
 
 def sq_gemm_fp8b(X_8, s_x, W_8, s_w, M: int, N: int, K: int, Y: torch.Tensor, stream=None) -> None:
     _rowmajor(Y, "Y", torch.bfloat16)
-    if tuple(Y.shape) != (M, N):
+    if Y.shape != (M, N):
         raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
     _check_codes(X_8, s_x, ("X_8", "s_x"), (M,), K, (M,))
     _check_codes(W_8, s_w, ("W_8", "s_w"), (N,), K, (-(-N // 128),))
-    _block_device(X_8, s_x, W_8, s_w, Y)
-    st = load().sq_gemm_fp8b(_ptr(X_8), _ptr(s_x), _ptr(W_8), _ptr(s_w), M, N, K, _ptr(Y), _ld(Y), _stream(stream))
+    dev = _block_device(X_8, s_x, W_8, s_w, Y)
+    st = load().sq_gemm_fp8b(X_8.data_ptr(), s_x.data_ptr(), W_8.data_ptr(), s_w.data_ptr(), M, N, K, Y.data_ptr(),
+                             _ld(Y), _raw_stream(stream, dev))
     _raise(st, "sq_gemm_fp8b")
 
 
@@ -540,12 +558,13 @@ def sq_linear_fp8b(X: torch.Tensor, W_8, s_w, N: int, Y: torch.Tensor, workspace
     _rowmajor(X, "X", torch.bfloat16)
     _rowmajor(Y, "Y", torch.bfloat16)
     M, K = X.shape
-    if tuple(Y.shape) != (M, N):
+    if Y.shape != (M, N):
         raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
     _check_codes(W_8, s_w, ("W_8", "s_w"), (N,), K, (-(-N // 128),))
-    _block_device(X, W_8, s_w, Y, workspace)
-    st = load().sq_linear_fp8b(_ptr(X), M, K, _ld(X), _ptr(W_8), _ptr(s_w), N, _ptr(Y), _ld(Y),
-                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    dev = _block_device(X, W_8, s_w, Y, workspace)
+    st = load().sq_linear_fp8b(X.data_ptr(), M, K, _ld(X), W_8.data_ptr(), s_w.data_ptr(), N, Y.data_ptr(), _ld(Y),
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _raw_stream(stream, dev))
     _raise(st, "sq_linear_fp8b")
 
 
@@ -566,10 +585,10 @@ def sq_route(logits: torch.Tensor, k: int, ids: torch.Tensor, weights: torch.Ten
     _expect(weights, "weights", torch.float32, T, k)
     if bias is not None:
         _expect(bias, "bias", torch.float32, E)
-    _block_device(logits, bias, ids, weights)
-    st = load().sq_route(_ptr(logits), int(logits.dtype == torch.bfloat16), T, E, _ld(logits), _ptr(bias),
-                         _SCORING[scoring], groups, keep_groups, group_top, k, int(renormalize), float(scale),
-                         _ptr(ids), _ptr(weights), _stream(stream))
+    dev = _block_device(logits, ids, weights, *(() if bias is None else (bias,)))
+    st = load().sq_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), T, E, _ld(logits),
+                         None if bias is None else bias.data_ptr(), _SCORING[scoring], groups, keep_groups, group_top, k, int(renormalize), float(scale),
+                         ids.data_ptr(), weights.data_ptr(), _raw_stream(stream, dev))
     _raise(st, "sq_route")
 
 
@@ -578,8 +597,9 @@ def sq_moe_dispatch(ids: torch.Tensor, E: int, offsets: torch.Tensor, pos: torch
     _expect(ids, "ids", torch.int32, T, k)
     _expect(offsets, "offsets", torch.int32, E + 1)
     _expect(pos, "pos", torch.int32, T, k)
-    _block_device(ids, offsets, pos)
-    _raise(load().sq_moe_dispatch(_ptr(ids), T, k, E, _ptr(offsets), _ptr(pos), _stream(stream)), "sq_moe_dispatch")
+    dev = _block_device(ids, offsets, pos)
+    st = load().sq_moe_dispatch(ids.data_ptr(), T, k, E, offsets.data_ptr(), pos.data_ptr(), _raw_stream(stream, dev))
+    _raise(st, "sq_moe_dispatch")
 
 
 def sq_moe_quant_fp8b(X: torch.Tensor, pos: torch.Tensor, X_8: torch.Tensor, s_x: torch.Tensor, stream=None) -> None:
@@ -588,8 +608,9 @@ def sq_moe_quant_fp8b(X: torch.Tensor, pos: torch.Tensor, X_8: torch.Tensor, s_x
     k = pos.shape[1]
     _expect(pos, "pos", torch.int32, T, k)
     _check_codes(X_8, s_x, ("X_8", "s_x"), (T * k,), K, (T * k,))
-    _block_device(X, pos, X_8, s_x)
-    st = load().sq_moe_quant_fp8b(_ptr(X), T, K, _ld(X), _ptr(pos), k, _ptr(X_8), _ptr(s_x), _stream(stream))
+    dev = _block_device(X, pos, X_8, s_x)
+    st = load().sq_moe_quant_fp8b(X.data_ptr(), T, K, _ld(X), pos.data_ptr(), k, X_8.data_ptr(), s_x.data_ptr(),
+                                  _raw_stream(stream, dev))
     _raise(st, "sq_moe_quant_fp8b")
 
 
@@ -599,23 +620,23 @@ def sq_moe_swiglu_fp8b(X_8, s_x, offsets, W13_8, s_w13, I: int, K: int, H_8, s_h
     _check_codes(X_8, s_x, ("X_8", "s_x"), (R,), K, (R,))
     _check_codes(W13_8, s_w13, ("W13_8", "s_w13"), (E, 2, I), K, (E, 2, -(-I // 128)))
     _check_codes(H_8, s_h, ("H_8", "s_h"), (R,), I, (R,))
-    _block_device(X_8, s_x, offsets, W13_8, s_w13, H_8, s_h)
-    st = load().sq_moe_swiglu_fp8b(_ptr(X_8), _ptr(s_x), _ptr(offsets), R, _ptr(W13_8), _ptr(s_w13), E, I, K,
-                                   _ptr(H_8), _ptr(s_h), _stream(stream))
+    dev = _block_device(X_8, s_x, offsets, W13_8, s_w13, H_8, s_h)
+    st = load().sq_moe_swiglu_fp8b(X_8.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R, W13_8.data_ptr(),
+                                   s_w13.data_ptr(), E, I, K, H_8.data_ptr(), s_h.data_ptr(), _raw_stream(stream, dev))
     _raise(st, "sq_moe_swiglu_fp8b")
 
 
 def sq_moe_gemm_fp8b(X_8, s_x, offsets, W_8, s_w, N: int, K: int, Y: torch.Tensor, stream=None) -> None:
     _rowmajor(Y, "Y", torch.bfloat16)
     R, E = X_8.shape[0], offsets.numel() - 1
-    if tuple(Y.shape) != (R, N):
+    if Y.shape != (R, N):
         raise ValueError(f"Y: expected shape {(R, N)}, got {tuple(Y.shape)}")
     _expect(offsets, "offsets", torch.int32, E + 1)
     _check_codes(X_8, s_x, ("X_8", "s_x"), (R,), K, (R,))
     _check_codes(W_8, s_w, ("W_8", "s_w"), (E, N), K, (E, -(-N // 128)))
-    _block_device(X_8, s_x, offsets, W_8, s_w, Y)
-    st = load().sq_moe_gemm_fp8b(_ptr(X_8), _ptr(s_x), _ptr(offsets), R, _ptr(W_8), _ptr(s_w), E, N, K, _ptr(Y),
-                                 _ld(Y), _stream(stream))
+    dev = _block_device(X_8, s_x, offsets, W_8, s_w, Y)
+    st = load().sq_moe_gemm_fp8b(X_8.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R, W_8.data_ptr(),
+                                 s_w.data_ptr(), E, N, K, Y.data_ptr(), _ld(Y), _raw_stream(stream, dev))
     _raise(st, "sq_moe_gemm_fp8b")
 
 
@@ -624,13 +645,13 @@ def sq_moe_combine(Z: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, Y:
     _rowmajor(Y, "Y", torch.bfloat16)
     T, k = pos.shape
     N = Z.shape[1]
-    if tuple(Y.shape) != (T, N):
+    if Y.shape != (T, N):
         raise ValueError(f"Y: expected shape {(T, N)}, got {tuple(Y.shape)}")
     _expect(pos, "pos", torch.int32, T, k)
     _expect(weights, "weights", torch.float32, T, k)
-    _block_device(Z, pos, weights, Y)
-    st = load().sq_moe_combine(_ptr(Z), Z.shape[0], _ld(Z), _ptr(pos), _ptr(weights), T, k, N, _ptr(Y),
-                               _ld(Y), _stream(stream))
+    dev = _block_device(Z, pos, weights, Y)
+    st = load().sq_moe_combine(Z.data_ptr(), Z.shape[0], _ld(Z), pos.data_ptr(), weights.data_ptr(), T, k, N,
+                               Y.data_ptr(), _ld(Y), _raw_stream(stream, dev))
     _raise(st, "sq_moe_combine")
 
 
@@ -640,16 +661,16 @@ def sq_experts_fp8b(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W
     _rowmajor(Y, "Y", torch.bfloat16)
     T, H = X.shape
     E, k = W2_8.shape[0], ids.shape[1]
-    if tuple(Y.shape) != (T, H):
+    if Y.shape != (T, H):
         raise ValueError(f"Y: expected shape {(T, H)}, got {tuple(Y.shape)}")
     _expect(ids, "ids", torch.int32, T, k)
     _expect(weights, "weights", torch.float32, T, k)
     _check_codes(W13_8, s_w13, ("W13_8", "s_w13"), (E, 2, I), H, (E, 2, -(-I // 128)))
     _check_codes(W2_8, s_w2, ("W2_8", "s_w2"), (E, H), I, (E, -(-H // 128)))
-    _block_device(X, ids, weights, W13_8, s_w13, W2_8, s_w2, Y, workspace)
-    st = load().sq_experts_fp8b(_ptr(X), T, H, _ld(X), _ptr(ids), _ptr(weights), k, _ptr(W13_8), _ptr(s_w13),
-                                _ptr(W2_8), _ptr(s_w2), E, I, _ptr(Y), _ld(Y), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+    dev = _block_device(X, ids, weights, W13_8, s_w13, W2_8, s_w2, Y, workspace)
+    st = load().sq_experts_fp8b(X.data_ptr(), T, H, _ld(X), ids.data_ptr(), weights.data_ptr(), k, W13_8.data_ptr(),
+                                s_w13.data_ptr(), W2_8.data_ptr(), s_w2.data_ptr(), E, I, Y.data_ptr(), _ld(Y),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     _raise(st, "sq_experts_fp8b")
 
 
