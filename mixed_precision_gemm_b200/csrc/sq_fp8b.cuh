@@ -87,13 +87,16 @@ __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__res
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * (QB_THREADS / 32) + (threadIdx.x >> 5); w < tasks; w += wpg) {
         const int64_t r = w / segs;
         const int c0 = static_cast<int>(w - r * segs) * (QB_SEG / 8) + lane;
+        int32_t dst = -1;                       // lane j: the row's j-th copy
         if (top > 0) {
-            bool any = false;
-            for (int j = 0; j < top; ++j) any |= pos[r * top + j] >= 0;
-            if (!any) continue;
+            if (lane < top) dst = pos[r * top + lane];
+            if (dst >= rows_out) dst = -1;
+            if (!__any_sync(0xFFFFFFFFu, dst >= 0)) continue;
         }
         const uint16_t *row = X + r * ldx;
         uint4 v[QB_CHUNKS];
+        uint2 q[QB_CHUNKS];
+        float sc[QB_CHUNKS];
 #pragma unroll
         for (int i = 0; i < QB_CHUNKS; ++i) {
             const int c = c0 + 32 * i;
@@ -106,13 +109,17 @@ __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__res
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const BlockScale b = block_scale(__uint_as_float(m << 16));
-            const uint2 q = block_codes(v[i], b);
-            const int n = top > 0 ? top : 1;
-            for (int j = 0; j < n; ++j) {
-                const int64_t d = top > 0 ? pos[r * top + j] : r;
-                if (d < 0 || d >= rows_out) continue;
-                if (8 * c < k_pad) *reinterpret_cast<uint2 *>(X_8 + d * k_pad + 8 * c) = q;
-                if ((lane & 15) == 0 && (c >> 4) < s_ld) s_x[d * s_ld + (c >> 4)] = b.s;
+            q[i] = block_codes(v[i], b);
+            sc[i] = b.s;
+        }
+        for (int j = 0; j < (top > 0 ? top : 1); ++j) {
+            const int64_t d = top > 0 ? __shfl_sync(0xFFFFFFFFu, dst, j) : r;
+            if (d < 0) continue;
+#pragma unroll
+            for (int i = 0; i < QB_CHUNKS; ++i) {
+                const int c = c0 + 32 * i;
+                if (8 * c < k_pad) *reinterpret_cast<uint2 *>(X_8 + d * k_pad + 8 * c) = q[i];
+                if ((lane & 15) == 0 && (c >> 4) < s_ld) s_x[d * s_ld + (c >> 4)] = sc[i];
             }
         }
     }

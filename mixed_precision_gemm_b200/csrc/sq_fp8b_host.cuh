@@ -270,6 +270,9 @@ sq_status route_impl(const void *logits, int logits_bf16, int64_t T, int64_t E, 
     a.keep = static_cast<int>(keep);
     a.group_top = static_cast<int>(group_top);
     a.bf16 = logits_bf16;
+    // 16-byte loads: whole lanes of 4 fp32 or 8 bf16 logits, every row on a 16-byte boundary
+    const int lane_logits = logits_bf16 ? 8 : 4;
+    a.vec = E % (32 * lane_logits) == 0 && (E & (E - 1)) == 0 && ldl % lane_logits == 0;
     a.sigmoid = sigmoid;
     a.renorm = renorm;
     a.scale = scale;

@@ -28,14 +28,15 @@ constexpr int RT_WARPS = 4;
 // error, the warp does the token again in fp64.  Scores that are logits
 // are exact and never need it.
 //
-// One warp per token, expert e in lane e % 32.  A choice is one integer
-// maximum over the warp (order-preserving keys) and one minimum for the index.
+// One warp per token, V = E / 32 rounded up to a power of two consecutive experts
+// per lane.  A choice is one integer maximum over the warp (order-preserving keys)
+// and a ballot for the lowest lane that has it.
 struct RouteArgs {
     const void *logits;
     int64_t T, ld;
     const float *bias;
     int E, top, groups, keep, group_top;
-    int bf16, sigmoid, renorm;
+    int bf16, sigmoid, renorm, vec;
     float scale;
     int32_t *ids;
     float *weights;
@@ -65,9 +66,6 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k)
     return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
-__device__ __forceinline__ float exp_t(float v) { return expf(v); }
-__device__ __forceinline__ double exp_t(double v) { return exp(v); }
-
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v)
 {
@@ -77,109 +75,149 @@ __device__ __forceinline__ T warp_sum(T v)
 }
 
 // A score closer than this to another one decides nothing in fp32 (relative to
-// the larger of 1 and the score): exponentials, the sum of up to 512 of them, the
-// quotient and the bias leave less than 2^-18.
+// the larger of 1 and the score): the hardware exponential of a logit (2^-22, and
+// 2^-24 of the argument's size, which e^-size outweighs), the sum of up to 512 of
+// them, the reciprocal and the bias leave less than 2^-18 on either side.
 __device__ __forceinline__ bool too_close(float a, float b) { return a - b <= 7.62939453125e-6f * fmaxf(1.0f, fmaxf(fabsf(a), fabsf(b))); }
 __device__ __forceinline__ bool too_close(double, double) { return false; }
+
+__device__ __forceinline__ float finite_logit(float l) { return l != l ? -INFINITY : fminf(l, 3.402823466e38f); }
 
 __device__ __forceinline__ float load_logit(const RouteArgs &a, int64_t t, int e)
 {
     const float l = a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.logits)[t * a.ld + e]) << 16)
                            : static_cast<const float *>(a.logits)[t * a.ld + e];
-    return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+    return finite_logit(l);
 }
 
+__device__ __forceinline__ float fast_exp(float v) { return __expf(v); }
+__device__ __forceinline__ double fast_exp(double v) { return exp(v); }
+__device__ __forceinline__ float fast_inverse(float v) { return __fdividef(1.0f, v); }
+__device__ __forceinline__ double fast_inverse(double v) { return 1.0 / v; }
+
 // Chosen experts of one token: lane j < top holds the j-th (-1: none).  Returns
-// false (all lanes) where fp32 scores cannot decide.  stat receives what p needs:
-// the largest logit and the sum of exponentials (softmax).
+// false (all lanes) where fp32 scores cannot decide.  lmax and sum receive what p
+// needs: the largest logit and the sum of exponentials (softmax).
+// Lane l holds experts [l V, l V + V): of equal keys the lowest lane's first one
+// is the lowest expert.
 template <typename T, int V>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], bool by_logit, int lane, int &mine, float &lmax, T &sum)
 {
     using Key = decltype(key_of(T()));
     if (!a.sigmoid) {
-        float mx = -INFINITY;
+        float mx = l[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) mx = fmaxf(mx, l[i]);
+        for (int i = 1; i < V; ++i) mx = fmaxf(mx, l[i]);
         lmax = value_of(warp_max(key_of(mx)));
         T s = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += l[i] == -INFINITY ? T(0) : exp_t(static_cast<T>(l[i]) - static_cast<T>(lmax));
+        for (int i = 0; i < V; ++i) s += l[i] == -INFINITY ? T(0) : fast_exp(static_cast<T>(l[i]) - static_cast<T>(lmax));
         sum = warp_sum(s);
     }
+    const T inv = a.sigmoid ? T(0) : fast_inverse(sum);
     Key key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
+        const int e = lane * V + i;
         T v = static_cast<T>(l[i]);
         if (!by_logit) {
-            v = a.sigmoid ? T(1) / (T(1) + exp_t(-v)) : exp_t(v - static_cast<T>(lmax)) / sum;
-            if (a.bias && e < a.E) v += static_cast<T>(a.bias[e]);
+            v = a.sigmoid ? fast_inverse(T(1) + fast_exp(-v)) : fast_exp(v - static_cast<T>(lmax)) * inv;
+            if (a.bias && e < a.E) v += static_cast<T>(__ldg(a.bias + e));
         }
         key[i] = l[i] == -INFINITY ? Key(0) : key_of(v);
     }
     bool sure = true;
     if (a.groups > 1) {
         const int per = a.E / a.groups;
-        Key gkey = 0;   // lane g: group g's worth
-        for (int g = 0; g < a.groups; ++g) {
-            T worth = 0;
-            bool some = false;
-            int skip = -1;
-            for (int n = 0; n < a.group_top; ++n) {
-                Key best = 0;
-                int at = 0x7FFFFFFF;
+        const int span = per / V;                // lanes per group
+        // A group of whole lanes, as many as a power of two: its two best by exchanges
+        // inside the group.  gkey: what the lane's group counts (0: no expert left).
+        const bool by_lanes = per % V == 0 && (span & (span - 1)) == 0;
+        Key gkey = 0;
+        int group = lane;                        // whose worth gkey is
+        if (by_lanes) {
+            Key k1 = 0, k2 = 0;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e >= g * per && e < (g + 1) * per && e != skip && key[i] > best) { best = key[i]; at = e; }
-                }
-                const Key top = warp_max(best);
-                if (top == 0) break;
-                skip = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(best == top ? at : 0x7FFFFFFF)));
-                worth += value_of(top);
-                some = true;
+            for (int i = 0; i < V; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
             }
-            if (lane == g) gkey = some ? key_of(worth) : Key(0);
+            for (int o = 1; o < span; o <<= 1) {
+                const Key o1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
+                k2 = max(max(k2, o2), min(k1, o1));
+                k1 = max(k1, o1);
+            }
+            if (k1) gkey = a.group_top > 1 && k2 ? key_of(value_of(k1) + value_of(k2)) : k1;
+            group = lane / span;
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                T worth = 0;
+                bool some = false;
+                int skip = -1;
+                for (int n = 0; n < a.group_top; ++n) {
+                    Key best = 0;
+                    int at = 0x7FFFFFFF;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const int e = lane * V + i;
+                        if (e >= g * per && e < (g + 1) * per && e != skip && key[i] > best) { best = key[i]; at = e; }
+                    }
+                    const Key top = warp_max(best);
+                    if (top == 0) break;
+                    skip = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(best == top ? at : 0x7FFFFFFF)));
+                    worth += value_of(top);
+                    some = true;
+                }
+                if (lane == g) gkey = some ? key_of(worth) : Key(0);
+            }
         }
-        uint32_t open = 0;
+        uint32_t open = 0;                       // bit g: group g is kept
         T last = 0;
         for (int n = 0; n <= a.keep && n < a.groups; ++n) {
-            const Key best = warp_max((open >> lane) & 1u ? Key(0) : gkey);
+            const Key rest = (open >> group) & 1u ? Key(0) : gkey;
+            const Key best = warp_max(rest);
             if (best == 0) break;
             const T v = value_of(best);
             if (n == a.keep) {
                 if (!by_logit && too_close(last, v)) sure = false;
                 break;
             }
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, !((open >> lane) & 1u) && gkey == best);
-            open |= who & (0u - who);
+            const int who = __ffs(__ballot_sync(0xFFFFFFFFu, rest == best)) - 1;
+            open |= 1u << (by_lanes ? who / span : who);
             last = v;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E && !((open >> (e / per)) & 1u)) key[i] = 0;
+            const int e = lane * V + i;
+            if (e < a.E && !((open >> (by_lanes ? group : e / per)) & 1u)) key[i] = 0;
         }
     }
     mine = -1;
     T last = 0;
     for (int n = 0; n <= a.top; ++n) {
-        Key best = 0;
-        int at = 0x7FFFFFFF;
+        Key best = key[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) { best = key[i]; at = lane + 32 * i; }
+        for (int i = 1; i < V; ++i) best = max(best, key[i]);
         const Key top = warp_max(best);
         if (top == 0) break;
-        const T v = value_of(top);
-        if (n > 0 && !by_logit && too_close(last, v)) sure = false;
+        if (!by_logit) {
+            const T v = value_of(top);
+            if (n > 0 && too_close(last, v)) sure = false;
+            last = v;
+        }
         if (n == a.top) break;
-        const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(best == top ? at : 0x7FFFFFFF)));
-        if (lane == n) mine = e;
+        const int who = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == lane + 32 * i) key[i] = 0;
-        last = v;
+        for (int i = V - 1; i >= 0; --i)
+            if (key[i] == top) at = i;           // the first of them
+        const int e = __shfl_sync(0xFFFFFFFFu, lane * V + at, who);
+        if (lane == n) mine = e;
+        if (lane == who) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == at) key[i] = 0;
+        }
     }
     return sure;
 }
@@ -190,12 +228,30 @@ __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteArgs a)
     sqd::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
-    sqd::pdl_wait();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * RT_WARPS + (threadIdx.x >> 5);
+    sqd::pdl_wait();
     if (t >= a.T) return;
     float l[V];
+    if (a.vec) {
+        // the lane's V logits by 16-byte loads (every row starts on one, and E = 32 V)
+        uint32_t u[V];
+        const int n = a.bf16 ? V / 8 : V / 4;
+        const uint4 *row = static_cast<const uint4 *>(a.logits) + (t * a.ld + lane * V) / (a.bf16 ? 8 : 4);
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.E ? load_logit(a, t, lane + 32 * i) : -INFINITY;
+        for (int i = 0; i < (V + 3) / 4; ++i)
+            if (i < n) {
+                const uint4 v = row[i];
+                if (V >= 4) { u[(4 * i) % V] = v.x; u[(4 * i + 1) % V] = v.y; u[(4 * i + 2) % V] = v.z; u[(4 * i + 3) % V] = v.w; }
+            }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t w = a.bf16 ? ((i & 1) ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16) : u[i];
+            l[i] = finite_logit(__uint_as_float(w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = lane * V + i < a.E ? load_logit(a, t, lane * V + i) : -INFINITY;
+    }
     int mine;
     float lmax = 0.0f, sum = 1.0f;
     if (!choose<float, V>(a, l, by_logit, lane, mine, lmax, sum)) {
@@ -222,6 +278,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteArgs a)
 // gives out rows in order, 32 pairs at a time (lanes with the same expert rank
 // themselves by lane).  No atomics decide an order.
 constexpr int DP_WARPS = 32;
+constexpr int DP_UNROLL = 8;   // ids in flight per lane
 
 __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
                                                                  int32_t *__restrict__ offsets, int32_t *__restrict__ pos)
@@ -236,9 +293,16 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
     const int64_t per = ((pairs + DP_WARPS - 1) / DP_WARPS + 31) / 32 * 32;
     const int64_t lo = min(per * w, pairs), hi = min(lo + per, pairs);
     int32_t *mine = cnt + w * E;
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-        const int e = ids[i];
-        if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * DP_UNROLL) {
+        int e[DP_UNROLL];
+#pragma unroll
+        for (int u = 0; u < DP_UNROLL; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            e[u] = i < hi ? ids[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < DP_UNROLL; ++u)
+            if (e[u] >= 0 && e[u] < E) atomicAdd(mine + e[u], 1);
     }
     __syncthreads();
     // counts -> first row of every (warp, expert), relative to the expert
@@ -269,18 +333,28 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
     }
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = off[e];
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int e = i < hi ? ids[i] : -1;
-        if (e < 0 || e >= E) e = -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        int32_t r = -1;
-        if (e >= 0) r = off[e] + mine[e] + rank;
-        __syncwarp();
-        if (e >= 0 && rank == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (i < hi) pos[i] = r;
+    for (int e = lane; e < E; e += 32) mine[e] += off[e];
+    __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * DP_UNROLL) {
+        int e[DP_UNROLL];
+#pragma unroll
+        for (int u = 0; u < DP_UNROLL; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            e[u] = i < hi ? ids[i] : -1;
+            if (e[u] >= E) e[u] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < DP_UNROLL; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[u]);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            int32_t r = -1;
+            if (e[u] >= 0) r = mine[e[u]] + rank;
+            __syncwarp();
+            if (e[u] >= 0 && rank == 0) mine[e[u]] += __popc(same);
+            __syncwarp();
+            if (i < hi) pos[i] = r;
+        }
     }
 }
 
@@ -289,6 +363,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
 // the order of j, fp32, rounded once.  One thread per 8 columns; the rows of Z
 // that have no choice are never read.  Memory-bound: top + 1 rows of 2 N bytes.
 constexpr int CB_THREADS = 256;
+constexpr int CB_FLIGHT = 8;   // rows in flight per thread
 
 __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const uint16_t *__restrict__ Z, int64_t rows_z, int64_t ldz,
                                                              const int32_t *__restrict__ pos, const float *__restrict__ weights,
@@ -303,16 +378,27 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const uint16_t *__r
         const int64_t t = i / per;
         const int c = static_cast<int>(i - t * per) * 8;
         float acc[8] = {};
-        for (int j = 0; j < top; ++j) {
-            const int64_t r = pos[t * top + j];
-            if (r < 0 || r >= rows_z) continue;
-            const float w = weights[t * top + j];
-            const uint4 v = *reinterpret_cast<const uint4 *>(Z + r * ldz + c);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int j0 = 0; j0 < top; j0 += CB_FLIGHT) {
+            int32_t r[CB_FLIGHT];
+            float w[CB_FLIGHT];
+            uint4 v[CB_FLIGHT];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                acc[2 * q] = fmaf(w, __uint_as_float(u[q] << 16), acc[2 * q]);
-                acc[2 * q + 1] = fmaf(w, __uint_as_float(u[q] & 0xFFFF0000u), acc[2 * q + 1]);
+            for (int j = 0; j < CB_FLIGHT; ++j) {
+                r[j] = j0 + j < top ? pos[t * top + j0 + j] : -1;
+                w[j] = j0 + j < top ? weights[t * top + j0 + j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < CB_FLIGHT; ++j)
+                v[j] = r[j] >= 0 && r[j] < rows_z ? *reinterpret_cast<const uint4 *>(Z + r[j] * ldz + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < CB_FLIGHT; ++j) {
+                if (r[j] < 0 || r[j] >= rows_z) continue;
+                const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    acc[2 * q] = fmaf(w[j], __uint_as_float(u[q] << 16), acc[2 * q]);
+                    acc[2 * q + 1] = fmaf(w[j], __uint_as_float(u[q] & 0xFFFF0000u), acc[2 * q + 1]);
+                }
             }
         }
         uint32_t o[4];
