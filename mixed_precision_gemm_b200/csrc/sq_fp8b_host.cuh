@@ -140,17 +140,21 @@ sq_status launch_skinny_b(const DevInfo &di, const sqb::ProductArgs &a, cudaStre
     // Row chunks: at most one partial one per expert that has rows.
     const int64_t experts = a.offsets ? std::min<int64_t>(a.G, a.M) : 1;
     const int64_t tiles = (a.offsets ? a.M / C::MP + experts : (a.M + C::MP - 1) / C::MP) * a.nb;
-    // As many splits as fill the SMs' places once, if every expert had one chunk.
-    int64_t S = static_cast<int64_t>(C::PER_SM) * di.sms / std::max<int64_t>(1, experts * a.nb);
-    S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(S, sqb::SB_MAX_SPLITS), a.kb));
-    if (tiles * S > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld tiles", (long long)tiles);
+    const size_t smem = C::smem(a.G);
+    auto kern = sqb::product_skinny_kernel<C>;
+    int per_sm = 0;
+    SQ_TRY(kernel_setup(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, smem, per_sm, "block-scaled skinny set-up"));
+    // Splits: as many as fill the SMs' places once, if every expert had one chunk, and
+    // leave a CTA two blocks.
+    const int64_t places = static_cast<int64_t>(per_sm) * di.sms;
+    int64_t S = places / std::max<int64_t>(1, experts * a.nb);
+    S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(S, sqb::SB_MAX_SPLITS), a.kb / 2));
+    const int64_t grid = S > 1 ? tiles * S : std::min(tiles, places);
+    if (tiles > 0x3FFFFFFFll || grid > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld tiles", (long long)tiles);
     sqb::SkinnyBArgs sa;
     sa.p = a;
     sa.splits = static_cast<int>(S);
-    auto kern = sqb::product_skinny_kernel<C>;
-    int per_sm = 0;
-    SQ_TRY(kernel_setup(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, C::SMEM, per_sm, "block-scaled skinny set-up"));
-    const cudaError_t e = launch_k(kern, dim3(static_cast<unsigned>(tiles * S)), dim3(sqb::SB_THREADS), C::SMEM, stream,
+    const cudaError_t e = launch_k(kern, dim3(static_cast<unsigned>(grid)), dim3(sqb::SB_THREADS), smem, stream,
                                    static_cast<unsigned>(S), m_x, m_w, sa);
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled skinny launch");
 }

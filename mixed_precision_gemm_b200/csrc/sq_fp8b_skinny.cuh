@@ -9,17 +9,20 @@
 // weight row) add it, times sx[m,b] sw[b], to MP sums in registers.  sx sw of four
 // blocks at a time is a table in shared memory, read as broadcasts.
 //
-// The blocks of a tile are divided over the S <= 8 CTAs of a cluster, so that few
-// tiles still occupy every SM.  CTA r of the cluster owns the tile's rows of X
-// [r TP, (r + 1) TP), TP = ceil(MP / S): every CTA sends the owner its sums through
+// With enough tiles for every SM the kernel is persistent (S = 1): each CTA takes
+// every gridDim.x-th tile, its loads running ahead into the next tile while the
+// sums of the last one are stored.  With fewer, the blocks of a tile are divided
+// over the S <= 8 CTAs of a cluster (one tile per cluster).  The rows of X are then
+// dealt out to the CTAs in fours: every CTA sends each row's owner its sums through
 // distributed shared memory (the operand ring, free by then), and the owner adds
-// them in rank order and stores; in the SwiGLU form it has the 128 columns of h
-// that share a scale, and writes their codes.
+// them in rank order and stores.
+// SwiGLU: whoever stores a row of X has the 128 columns of h that share a scale, and
+// writes their codes.
 //
 // Memory-bound on the weights; two CTAs fit on an SM (one where the tile is
 // large), so that one loads while the other starts or finishes.
 //
-// Roles (6 warps): 0 loads (TMA), 1 issues the MMAs, 2..5 sums.
+// Roles (6 warps): 0 loads (TMA), 1 issues the MMAs, 2..5 sums and stores.
 #pragma once
 
 #include "sq_fp8b.cuh"
@@ -42,14 +45,16 @@ struct CfgSkinnyB {
     static constexpr int NB = 256 / COLS < 4 ? 256 / COLS : 4;   // TMEM buffers
     static constexpr int TMEM = NB * COLS <= 32 ? 32 : NB * COLS <= 64 ? 64 : NB * COLS <= 128 ? 128 : 256;
     static constexpr int OFF_TAB = NST * STAGE;                  // [2][4][MATS][MP] products of scales
-    static constexpr int OFF_MAX = OFF_TAB + 2 * 4 * MATS * MP * 4;   // [4 warps][MP] maxima
-    static constexpr int OFF_BAR = OFF_MAX + (SWIGLU ? 4 * MP * 4 : 0);
+    static constexpr int OFF_MAX = OFF_TAB + 2 * 4 * MATS * MP * 4;   // SwiGLU: [4 warps][MP] maxima, [3][MP] scale constants
+    static constexpr int OFF_BAR = OFF_MAX + (SWIGLU ? 7 * MP * 4 : 0);
     static constexpr int NBAR = 2 * NST + 2 * NB + 1;
-    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;          // TMEM address, abort flag, tile
-    static constexpr int SMEM = OFF_MISC + 32 + 1024;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;          // TMEM address, abort flag
+    static constexpr int OFF_PRE = OFF_MISC + 8;                 // first tile of each expert
+    static constexpr int smem(int G) { return OFF_PRE + 4 * (G + 1) + 768; }
     static_assert(STAGE % 1024 == 0, "swizzled tiles");
-    static_assert(MATS * (MP + SB_MAX_SPLITS - 1) * 512 <= NST * STAGE, "the exchanged sums fit in the ring");
-    static_assert(SMEM * PER_SM <= 232448 && TMEM * PER_SM <= 512, "an SM's share");
+    static_assert(MATS * (MP / 4 + SB_MAX_SPLITS - 1) * 2048 <= NST * STAGE, "the exchanged sums fit in the ring");
+    static_assert(smem(512) <= 232448, "shared memory");
+    static_assert((smem(256) + 1024) * PER_SM <= 233472 && TMEM * PER_SM <= 512, "an SM's share");
 };
 
 struct SkinnyBArgs {
@@ -57,38 +62,52 @@ struct SkinnyBArgs {
     int splits;
 };
 
-// Tile index -> expert, its first row of X in the tile and its end, weight tile.
-// Tiles of an expert: its row chunks fastest, so that those that share weight
-// rows run together.  Called by one whole warp; false behind the last tile.
-__device__ __forceinline__ bool skinny_tile(const ProductArgs &a, int mp, int t, int lane, int &g, int &m0, int &m_end, int &tn)
+// First tile of every expert, pre[0 .. G] (one warp).  An expert has a tile for
+// each MP of its rows and each 128 weight rows; its row chunks come fastest, so
+// that those that share weight rows run together.
+__device__ __forceinline__ void first_tiles(const ProductArgs &a, int mp, int lane, int32_t *pre)
 {
     int base = 0;
+    if (lane == 0) pre[0] = 0;
     for (int g0 = 0; g0 < a.G; g0 += 32) {
         int64_t lo = 0, hi = 0;
         if (g0 + lane < a.G) expert_rows(a, g0 + lane, lo, hi);
-        const int chunks = static_cast<int>((hi - lo + mp - 1) / mp);
-        int sum = chunks * a.nb;
-        const int mine = sum;
+        int sum = static_cast<int>((hi - lo + mp - 1) / mp) * a.nb;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += u;
         }
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, t < base + sum);
-        if (who) {
-            const int l = __ffs(who) - 1;
-            const int first = __shfl_sync(0xFFFFFFFFu, base + sum - mine, l);
-            const int c = __shfl_sync(0xFFFFFFFFu, chunks, l);
-            const int row = static_cast<int>(__shfl_sync(0xFFFFFFFFu, static_cast<int>(lo), l));
-            m_end = static_cast<int>(__shfl_sync(0xFFFFFFFFu, static_cast<int>(hi), l));
-            g = g0 + l;
-            tn = (t - first) / c;
-            m0 = row + (t - first) % c * mp;
-            return true;
-        }
+        if (g0 + lane < a.G) pre[g0 + lane + 1] = base + sum;
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    return false;
+}
+
+// Where tile t < pre[G] lies (one whole warp, growing t).
+struct SkinnyTile {
+    int g0 = 0;                  // first expert of the 32 that are looked at
+    int g, m0, m_end, tn;
+    __device__ void seek(const ProductArgs &a, int mp, const int32_t *pre, int t, int lane)
+    {
+        uint32_t who;
+        while ((who = __ballot_sync(0xFFFFFFFFu, g0 + lane < a.G && t < pre[g0 + lane + 1])) == 0) g0 += 32;
+        g = g0 + __ffs(who) - 1;
+        int64_t lo, hi;
+        expert_rows(a, g, lo, hi);
+        const int r = t - pre[g], chunks = (pre[g + 1] - pre[g]) / a.nb;
+        tn = r / chunks;
+        m0 = static_cast<int>(lo) + r % chunks * mp;
+        m_end = static_cast<int>(hi);
+    }
+};
+
+// The bytes of four lanes' words transposed: word of lane 4 i + j, byte k <-> lane 4 i + k, byte j.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t x, int lane)
+{
+    uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+    x = (lane & 1) ? __byte_perm(x, y, 0x3715) : __byte_perm(x, y, 0x6240);
+    y = __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+    return (lane & 2) ? __byte_perm(x, y, 0x3276) : __byte_perm(x, y, 0x5410);
 }
 
 template <class C>
@@ -96,6 +115,7 @@ __global__ void __launch_bounds__(SB_THREADS, C::PER_SM)
 product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const SkinnyBArgs args)
 {
     constexpr int MP = C::MP, NST = C::NST, NB = C::NB, MATS = C::MATS;
+    constexpr bool SWIGLU = C::SWIGLU;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = sqd::smem_u32(smem);
@@ -113,7 +133,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     const uint32_t drain = bar0 + 8u * (2 * NST + 2 * NB);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC + 4);
-    int *where = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);   // expert, first row, end, weight tile, any
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + C::OFF_PRE);
     auto stage = [&](int s) { return sbase + s * C::STAGE; };
 
     if (threadIdx.x == 0) {
@@ -137,51 +157,42 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         sqd::tmem_relinquish();
     }
     sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
-    if (warp == 0) {
-        int g = 0, m0 = 0, m_end = 0, tn = 0;
-        const bool any = skinny_tile(p, MP, static_cast<int>(blockIdx.x) / S, lane, g, m0, m_end, tn);
-        if (lane == 0) {
-            where[0] = g;
-            where[1] = m0;
-            where[2] = m_end;
-            where[3] = tn;
-            where[4] = any;
-        }
-    }
+    if (warp == 0) first_tiles(p, MP, lane, pre);
     sqd::tc_fence_before();
     __syncthreads();
     sqd::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int g = where[0], m0 = where[1], m_end = where[2], tn = where[3];
-    const bool any = where[4] != 0;   // the same in every CTA of the cluster
-    if (!any) {
-        if (warp == 1) sqd::tmem_dealloc(tmem, C::TMEM);
-        return;
-    }
+    const int tiles = pre[p.G];
+    // Tiles t0, t0 + step, ..: a cluster has one at most (the host's grid covers them all then).
+    const int t0 = static_cast<int>(blockIdx.x) / S, step = S > 1 ? 0x40000000 : static_cast<int>(gridDim.x);
     const int b_lo = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
     const int nblk = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S) - b_lo;
+    SkinnyTile tile;
 
-    float2 acc[MATS][MP / 2];
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            int s = 0, last = -1;
-            uint32_t ph = 0, last_ph = 0;
-            bool ok = true;
-            for (int i = 0; i < nblk; ++i) {
-                if (!sqd::mbar_wait(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
-                sqd::mbar_arrive_expect_tx(full(s), C::STAGE);
-                const int x = (b_lo + i) * BLK;
+        int s = 0, last = -1;
+        uint32_t ph = 0, last_ph = 0;
+        bool ok = true;
+        for (int t = t0; t < tiles; t += step) {
+            tile.seek(p, MP, pre, t, lane);
+            if (lane == 0) {
+                for (int i = 0; ok && i < nblk; ++i) {
+                    if (!sqd::mbar_wait(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
+                    sqd::mbar_arrive_expect_tx(full(s), C::STAGE);
+                    const int x = (b_lo + i) * BLK;
 #pragma unroll
-                for (int mat = 0; mat < MATS; ++mat)
-                    sqd::tma_load_2d(stage(s) + mat * C::W_BYTES, &tm_w, full(s), x, (g * MATS + mat) * p.N + tn * 128);
-                sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), x, m0);
-                last = s;
-                last_ph = ph;
-                if (++s == NST) { s = 0; ph ^= 1u; }
+                    for (int mat = 0; mat < MATS; ++mat)
+                        sqd::tma_load_2d(stage(s) + mat * C::W_BYTES, &tm_w, full(s), x, (tile.g * MATS + mat) * p.N + tile.tn * 128);
+                    sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), x, tile.m0);
+                    last = s;
+                    last_ph = ph;
+                    if (++s == NST) { s = 0; ph ^= 1u; }
+                }
             }
-            if (!ok && last >= 0) sqd::mbar_drain(full(last), last_ph);
+            __syncwarp();
         }
+        if (!ok && last >= 0) sqd::mbar_drain(full(last), last_ph);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
@@ -189,21 +200,23 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             int s = 0, j = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true;
-            for (int i = 0; i < nblk; ++i) {
-                const uint64_t ad = sqd::make_sw128_desc(stage(s));
-                const uint64_t bd = sqd::make_sw128_desc(stage(s) + MATS * C::W_BYTES);
-                if (!sqd::mbar_wait(full(s), ph, abort_flag, SITE_SB_MMA) ||
-                    !sqd::mbar_wait(bempty(j), bph ^ 1u, abort_flag, SITE_SB_MMA)) { ok = false; break; }
-                sqd::tc_fence_after();
+            for (int t = t0; ok && t < tiles; t += step) {
+                for (int i = 0; i < nblk; ++i) {
+                    const uint64_t ad = sqd::make_sw128_desc(stage(s));
+                    const uint64_t bd = sqd::make_sw128_desc(stage(s) + MATS * C::W_BYTES);
+                    if (!sqd::mbar_wait(full(s), ph, abort_flag, SITE_SB_MMA) ||
+                        !sqd::mbar_wait(bempty(j), bph ^ 1u, abort_flag, SITE_SB_MMA)) { ok = false; break; }
+                    sqd::tc_fence_after();
 #pragma unroll
-                for (int mat = 0; mat < MATS; ++mat)
+                    for (int mat = 0; mat < MATS; ++mat)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sqd::mma_f8(tmem + j * C::COLS + mat * MP, ad + mat * (C::W_BYTES >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                sqd::mma_commit(bfull(j));
-                sqd::mma_commit(empty(s));
-                if (++s == NST) { s = 0; ph ^= 1u; }
-                if (++j == NB) { j = 0; bph ^= 1u; }
+                        for (int k = 0; k < 4; ++k)
+                            sqd::mma_f8(tmem + j * C::COLS + mat * MP, ad + mat * (C::W_BYTES >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                    sqd::mma_commit(bfull(j));
+                    sqd::mma_commit(empty(s));
+                    if (++s == NST) { s = 0; ph ^= 1u; }
+                    if (++j == NB) { j = 0; bph ^= 1u; }
+                }
             }
             if (!ok) {
                 sqd::mma_commit(drain);
@@ -211,132 +224,216 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             }
         }
     } else {
-        // ------------------------------------------------------------ sums
-        // (a wait that gave up does not leave the loop, so that all four warps keep
-        // meeting at the table's barrier; the tile is not stored then)
+        // ------------------------------------------------------------ sums and stores
+        // (a wait that gave up does not leave the loops, so that all four warps keep
+        // meeting at barrier 1; nothing is stored then)
         const int et = threadIdx.x - 64;
+        const int wr = (warp & 3) * 32 + lane;   // the thread's weight row: its TMEM lane
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll
-        for (int mat = 0; mat < MATS; ++mat)
-#pragma unroll
-            for (int c = 0; c < MP / 2; ++c) acc[mat][c] = make_float2(0.0f, 0.0f);
         float *tab = reinterpret_cast<float *>(smem + C::OFF_TAB);
-        const bool row_ok = et < MP && m0 + et < m_end;
-        const float4 *sx_p = reinterpret_cast<const float4 *>(p.s_x + static_cast<int64_t>(row_ok ? m0 + et : 0) * p.s_ld);
-        const float4 *sw_p = reinterpret_cast<const float4 *>(p.s_w + (static_cast<int64_t>(g) * MATS * p.nb + tn) * p.s_ld);
+        float *wmax = reinterpret_cast<float *>(smem + C::OFF_MAX);
         const int sw_up = p.nb * p.s_ld / 4;    // the up matrix's scales behind the gate's
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 sx4 = z, sw4[MATS];
-        auto fetch = [&](int q) {
-            sx4 = row_ok ? __ldg(sx_p + q) : z;
-#pragma unroll
-            for (int mat = 0; mat < MATS; ++mat) sw4[mat] = __ldg(sw_p + mat * sw_up + q);
-        };
-        fetch(b_lo >> 2);
-        int j = 0;
+        int j = 0, group = 0;
         uint32_t bph = 0;
-        for (int i = 0; i < nblk; ++i) {
-            const int b = b_lo + i, q = b >> 2;
-            float *tq = tab + (q & 1) * (4 * MATS * MP);
-            if (i == 0 || (b & 3) == 0) {
-                if (et < MP) {
+        for (int t = t0; t < tiles; t += step) {
+            tile.seek(p, MP, pre, t, lane);
+            const bool row_ok = et < MP && tile.m0 + et < tile.m_end;
+            const float4 *sx_p = reinterpret_cast<const float4 *>(p.s_x + static_cast<int64_t>(row_ok ? tile.m0 + et : 0) * p.s_ld);
+            const float4 *sw_p = reinterpret_cast<const float4 *>(p.s_w + (static_cast<int64_t>(tile.g) * MATS * p.nb + tile.tn) * p.s_ld);
+            float4 sx4 = z, sw4[MATS];
+            auto fetch = [&](int q) {
+                sx4 = row_ok ? __ldg(sx_p + q) : z;
 #pragma unroll
-                    for (int mat = 0; mat < MATS; ++mat) {
-                        tq[(0 * MATS + mat) * MP + et] = sx4.x * sw4[mat].x;
-                        tq[(1 * MATS + mat) * MP + et] = sx4.y * sw4[mat].y;
-                        tq[(2 * MATS + mat) * MP + et] = sx4.z * sw4[mat].z;
-                        tq[(3 * MATS + mat) * MP + et] = sx4.w * sw4[mat].w;
-                    }
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (((q + 1) << 2) < b_lo + nblk) fetch(q + 1);
-            }
-            sqd::mbar_wait(bfull(j), bph, abort_flag, SITE_SB_EPI);
-            sqd::tc_fence_after();
-            const float4 *tb = reinterpret_cast<const float4 *>(tq + (b & 3) * MATS * MP);
-#pragma unroll
-            for (int ch = 0; ch < C::COLS / 16; ++ch) {
-                uint32_t v[16];
-                sqd::tmem_ld_32x32b_x16(tl + j * C::COLS + 16 * ch, v);
-                sqd::tmem_wait_ld_dep1(v);
-                if (ch + 1 == C::COLS / 16) {
-                    sqd::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) sqd::mbar_arrive(bempty(j));
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 s = tb[4 * ch + c];
-                    float2 &a0 = acc[ch * 16 / MP][(ch * 16 % MP) / 2 + 2 * c], &a1 = acc[ch * 16 / MP][(ch * 16 % MP) / 2 + 2 * c + 1];
-                    a0 = __ffma2_rn(make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), make_float2(s.x, s.y), a0);
-                    a1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), make_float2(s.z, s.w), a1);
-                }
-            }
-            if (++j == NB) { j = 0; bph ^= 1u; }
-        }
-    }
-
-    // ---------------------------------------------------------------- exchange and store
-    __syncwarp();
-    sqd::fence_proxy_async_smem();   // the ring, filled by TMA and read by the MMAs, is written by threads below
-    sqd::tc_fence_before();
-    if (S > 1) sqd::cluster_sync();  // every MMA of the cluster is complete
-    else __syncthreads();
-    const int TP = (MP + S - 1) / S;
-    const int et = static_cast<int>(threadIdx.x) - 64;
-    if (warp >= 2) {
-        // sums of row of X c to its owner: [mat][source][row of X][weight row]
-        const int wr = (warp & 3) * 32 + lane;   // the thread's TMEM lane
-        int owner = 0, cl = 0;
-#pragma unroll
-        for (int c = 0; c < MP; ++c) {
-            const uint32_t off = static_cast<uint32_t>(((rank * TP + cl) * 128 + wr) * 4);
-            const uint32_t dst = sqd::map_to_cta(sbase + off, static_cast<uint32_t>(owner));
+                for (int mat = 0; mat < MATS; ++mat) sw4[mat] = __ldg(sw_p + mat * sw_up + q);
+            };
+            fetch(b_lo >> 2);
+            float2 acc[MATS][MP / 2];
 #pragma unroll
             for (int mat = 0; mat < MATS; ++mat)
-                sqd::st_cluster_f32(dst + static_cast<uint32_t>(mat * S * TP * 512), (c & 1) ? acc[mat][c / 2].y : acc[mat][c / 2].x);
-            if (++cl == TP) { cl = 0; ++owner; }
-        }
-    }
-    if (S > 1) sqd::cluster_sync();  // all sums delivered
-    else __syncthreads();
-    if (warp >= 2 && !*abort_flag) {
-        float *red = reinterpret_cast<float *>(smem);
-        const int n = tn * 128 + et;
-        const int rows = min(min(TP, MP - rank * TP), m_end - m0 - rank * TP);   // owned rows that exist
-        const int64_t mr = m0 + rank * TP;
-        if constexpr (!C::SWIGLU) {
-            for (int cl = 0; cl < rows; ++cl) {
-                float s = 0.0f;
-                for (int src = 0; src < S; ++src) s += red[(src * TP + cl) * 128 + et];
-                if (n < p.N) p.Y[(mr + cl) * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-            }
-        } else {
-            float *wmax = reinterpret_cast<float *>(smem + C::OFF_MAX);
-            for (int cl = 0; cl < rows; ++cl) {
-                float gt = 0.0f, up = 0.0f;
-                for (int src = 0; src < S; ++src) {
-                    gt += red[(src * TP + cl) * 128 + et];
-                    up += red[((S + src) * TP + cl) * 128 + et];
+#pragma unroll
+                for (int c = 0; c < MP / 2; ++c) acc[mat][c] = make_float2(0.0f, 0.0f);
+            float *tq = tab;
+            for (int i = 0; i < nblk; ++i) {
+                const int b = b_lo + i, q = b >> 2;
+                if (i == 0 || (b & 3) == 0) {
+                    tq = tab + (group++ & 1) * (4 * MATS * MP);
+                    if (et < MP) {
+#pragma unroll
+                        for (int mat = 0; mat < MATS; ++mat) {
+                            tq[(0 * MATS + mat) * MP + et] = sx4.x * sw4[mat].x;
+                            tq[(1 * MATS + mat) * MP + et] = sx4.y * sw4[mat].y;
+                            tq[(2 * MATS + mat) * MP + et] = sx4.z * sw4[mat].z;
+                            tq[(3 * MATS + mat) * MP + et] = sx4.w * sw4[mat].w;
+                        }
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (((q + 1) << 2) < b_lo + nblk) fetch(q + 1);
                 }
-                const float h = n < p.N ? silu_mul(gt, up) : 0.0f;
-                red[cl * 128 + et] = h;
-                const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h)));
-                if (lane == 0) wmax[(warp - 2) * MP + cl] = __uint_as_float(m);
+                sqd::mbar_wait(bfull(j), bph, abort_flag, SITE_SB_EPI);
+                sqd::tc_fence_after();
+                const float4 *tb = reinterpret_cast<const float4 *>(tq + (b & 3) * MATS * MP);
+#pragma unroll
+                for (int ch = 0; ch < C::COLS / 16; ++ch) {
+                    uint32_t v[16];
+                    sqd::tmem_ld_32x32b_x16(tl + j * C::COLS + 16 * ch, v);
+                    sqd::tmem_wait_ld_dep1(v);
+                    if (ch + 1 == C::COLS / 16) {
+                        sqd::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) sqd::mbar_arrive(bempty(j));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 s = tb[4 * ch + c];
+                        float2 &a0 = acc[ch * 16 / MP][(ch * 16 % MP) / 2 + 2 * c], &a1 = acc[ch * 16 / MP][(ch * 16 % MP) / 2 + 2 * c + 1];
+                        a0 = __ffma2_rn(make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), make_float2(s.x, s.y), a0);
+                        a1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), make_float2(s.z, s.w), a1);
+                    }
+                }
+                if (++j == NB) { j = 0; bph ^= 1u; }
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            // codes of four columns per thread: 32 threads a row, four rows at a time
-            for (int cl = et >> 5; cl < rows; cl += 4) {
-                const float mx = fmaxf(fmaxf(wmax[cl], wmax[MP + cl]), fmaxf(wmax[2 * MP + cl], wmax[3 * MP + cl]));
-                const BlockScale bs = block_scale(mx);
-                const float4 h = reinterpret_cast<const float4 *>(red + cl * 128)[lane];
-                *reinterpret_cast<uint32_t *>(p.H_8 + (mr + cl) * p.h_pad + tn * 128 + 4 * lane) =
-                    codes2(h.x, h.y, bs) | (codes2(h.z, h.w, bs) << 16);
-                if (lane == 0) p.s_h[(mr + cl) * p.h_ld + tn] = bs.s;
-                if (tn == p.nb - 1 && p.nb + lane < p.h_ld) p.s_h[(mr + cl) * p.h_ld + p.nb + lane] = 0.0f;
+            const int n = tile.tn * 128 + wr;
+            const int64_t m0 = tile.m0;
+            int rows = min(MP, tile.m_end - tile.m0);        // rows of X in the tile
+            if (*abort_flag) rows = 0;
+            if (S == 1) {
+                if constexpr (!SWIGLU) {
+                    // Lanes 2 i and 2 i + 1 pair up: the even one stores row c, the odd one row c + 1, two
+                    // columns each.
+#pragma unroll
+                    for (int c = 0; c < MP; c += 2) {
+                        const float2 a = acc[0][c / 2];
+                        const float o = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? a.x : a.y, 1);
+                        const __nv_bfloat162 y2 = (lane & 1) ? __floats2bfloat162_rn(o, a.y) : __floats2bfloat162_rn(a.x, o);
+                        const int r = c + (lane & 1);
+                        if (r < rows && n < p.N) *reinterpret_cast<__nv_bfloat162 *>(p.Y + (m0 + r) * p.ldy + (n & ~1)) = y2;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < MP / 2; ++c) {
+                        const float2 gt = acc[0][c], up = acc[MATS - 1][c];
+                        const float2 h = n < p.N ? make_float2(silu_mul(gt.x, up.x), silu_mul(gt.y, up.y)) : make_float2(0.0f, 0.0f);
+                        acc[0][c] = h;
+                        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h.x)));
+                        const uint32_t my = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h.y)));
+                        if (lane == 0) *reinterpret_cast<float2 *>(wmax + (warp & 3) * MP + 2 * c) = make_float2(__uint_as_float(mx), __uint_as_float(my));
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    float *consts = wmax + 4 * MP;   // of each row's scale: its inverse, its negative, the factor of tiny ones
+                    if (et < MP) {
+                        const BlockScale bs = block_scale(fmaxf(fmaxf(wmax[et], wmax[MP + et]), fmaxf(wmax[2 * MP + et], wmax[3 * MP + et])));
+                        uint32_t inv, neg, hi;
+                        sqq::f2_unpack(bs.rs.inv2, inv, hi);
+                        sqq::f2_unpack(bs.rs.negs2, neg, hi);
+                        consts[et] = bs.zero ? 1.0f : __uint_as_float(inv);    // (1: zeros of either sign to code 0)
+                        consts[MP + et] = bs.zero ? -1.0f : __uint_as_float(neg);
+                        consts[2 * MP + et] = bs.up ? sqq::kUpScale : 1.0f;
+                        if (et < rows) {
+                            p.s_h[(m0 + et) * p.h_ld + tile.tn] = bs.s;
+                            if (tile.tn == p.nb - 1)
+                                for (int q = p.nb; q < p.h_ld; ++q) p.s_h[(m0 + et) * p.h_ld + q] = 0.0f;
+                        }
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                    for (int c = 0; c < MP; c += 4) {
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 h = acc[0][c / 2 + k], inv = *reinterpret_cast<const float2 *>(consts + c + 2 * k);
+                            const float2 neg = *reinterpret_cast<const float2 *>(consts + MP + c + 2 * k);
+                            const float2 v = __fmul2_rn(h, *reinterpret_cast<const float2 *>(consts + 2 * MP + c + 2 * k));
+                            const float2 q0 = __fmul2_rn(v, inv);
+                            const float2 q1 = __ffma2_rn(__ffma2_rn(q0, neg, v), inv, q0);
+                            w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q1, __NV_SATFINITE, __NV_E4M3)) << (16 * k);
+                        }
+                        w = transpose_bytes(w, lane);
+                        const int r = c + (lane & 3);
+                        if (r < rows) *reinterpret_cast<uint32_t *>(p.H_8 + (m0 + r) * p.h_pad + tile.tn * 128 + (wr & ~3)) = w;
+                    }
+                }
+            } else {
+                // ---------------------------------------------------- exchange over the cluster
+                sqd::fence_proxy_async_smem();   // the ring, filled by TMA and read by the MMAs, is written by threads below
+                sqd::tc_fence_before();
+                sqd::cluster_sync();             // every MMA of the cluster is complete
+                // rows of X in fours, TG of them per owner: [mat][source][four][weight row]
+                const int TG = (MP / 4 + S - 1) / S;
+                int owner = 0, gl = 0;
+#pragma unroll
+                for (int c = 0; c < MP / 4; ++c) {
+                    const uint32_t dst = sqd::map_to_cta(sbase + static_cast<uint32_t>(((rank * TG + gl) * 128 + wr) * 16), static_cast<uint32_t>(owner));
+#pragma unroll
+                    for (int mat = 0; mat < MATS; ++mat) {
+                        const float2 a = acc[mat][2 * c], b2 = acc[mat][2 * c + 1];
+                        sqd::st_cluster_v4(dst + static_cast<uint32_t>(mat * S * TG * 2048), __float_as_uint(a.x), __float_as_uint(a.y),
+                                           __float_as_uint(b2.x), __float_as_uint(b2.y));
+                    }
+                    if (++gl == TG) { gl = 0; ++owner; }
+                }
+                sqd::cluster_sync();             // all sums delivered
+                float4 *red = reinterpret_cast<float4 *>(smem);
+                const int r0 = rank * TG * 4;                       // owned rows of the tile: r0 ..
+                const int mine = min(4 * TG, rows - r0);
+                for (int f = 0; 4 * f < mine; ++f) {
+                    float4 sum[MATS];
+#pragma unroll
+                    for (int mat = 0; mat < MATS; ++mat) {
+                        sum[mat] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int src = 0; src < S; ++src) {
+                            const float4 v = red[((mat * S + src) * TG + f) * 128 + et];
+                            sum[mat].x += v.x;
+                            sum[mat].y += v.y;
+                            sum[mat].z += v.z;
+                            sum[mat].w += v.w;
+                        }
+                    }
+                    const int nn = tile.tn * 128 + et;
+                    if constexpr (!SWIGLU) {
+                        const float y[4] = {sum[0].x, sum[0].y, sum[0].z, sum[0].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (4 * f + k < mine && nn < p.N)
+                                p.Y[(m0 + r0 + 4 * f + k) * p.ldy + nn] = __bfloat16_as_ushort(__float2bfloat16_rn(y[k]));
+                    } else {
+                        const bool in = nn < p.N;
+                        const float4 gt = sum[0], up = sum[MATS - 1];
+                        const float h[4] = {in ? silu_mul(gt.x, up.x) : 0.0f, in ? silu_mul(gt.y, up.y) : 0.0f,
+                                            in ? silu_mul(gt.z, up.z) : 0.0f, in ? silu_mul(gt.w, up.w) : 0.0f};
+                        red[f * 128 + et] = make_float4(h[0], h[1], h[2], h[3]);   // (source 0's gate sums are used up)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[k])));
+                            if (lane == 0) wmax[(warp - 2) * MP + 4 * f + k] = __uint_as_float(m);
+                        }
+                    }
+                }
+                if constexpr (SWIGLU) {
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    const float *hs = reinterpret_cast<const float *>(smem);   // [four][column][row of the four]
+                    for (int r = et >> 5; r < mine; r += 4) {       // a warp per row, four columns per lane
+                        const BlockScale bs = block_scale(fmaxf(fmaxf(wmax[r], wmax[MP + r]), fmaxf(wmax[2 * MP + r], wmax[3 * MP + r])));
+                        const float *h = hs + ((r >> 2) * 128 + 4 * lane) * 4 + (r & 3);
+                        *reinterpret_cast<uint32_t *>(p.H_8 + (m0 + r0 + r) * p.h_pad + tile.tn * 128 + 4 * lane) =
+                            codes2(h[0], h[4], bs) | (codes2(h[8], h[12], bs) << 16);
+                        if (lane == 0) p.s_h[(m0 + r0 + r) * p.h_ld + tile.tn] = bs.s;
+                        if (tile.tn == p.nb - 1 && p.nb + lane < p.h_ld) p.s_h[(m0 + r0 + r) * p.h_ld + p.nb + lane] = 0.0f;
+                    }
+                }
             }
         }
     }
+    __syncwarp();
+    if (S > 1) {
+        if (warp < 2 && t0 < tiles) {   // the other warps have met there
+            sqd::tc_fence_before();
+            sqd::cluster_sync();
+            sqd::cluster_sync();
+        }
+    }
+    sqd::tc_fence_before();
+    __syncthreads();
     if (warp == 1) {
         sqd::tc_fence_after();
         sqd::tmem_dealloc(tmem, C::TMEM);
