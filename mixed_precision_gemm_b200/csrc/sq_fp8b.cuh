@@ -132,8 +132,9 @@ __global__ void __launch_bounds__(256) weight_blocks_kernel(const uint16_t *__re
                                                             int64_t stride_g, int k_pad, int s_ld,
                                                             uint8_t *__restrict__ W_8, float *__restrict__ s_w)
 {
+    // (no early start of the next kernel: products fetch weights before they wait for
+    // their predecessors)
     __shared__ uint32_t red[8];
-    sqd::pdl_launch_dependents();
     const int kb = blockIdx.x, nb = blockIdx.y;
     const int64_t g = blockIdx.z;
     const int c = kb * 16 + (threadIdx.x & 15);

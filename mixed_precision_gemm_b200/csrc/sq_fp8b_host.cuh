@@ -171,7 +171,7 @@ sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
     if (rows <= 32) return launch_skinny_b<sqb::CfgSkinnyB<32, SWIGLU, SWIGLU ? 3 : 5, 2>>(di, a, stream);
     if constexpr (SWIGLU) return launch_skinny_b<sqb::CfgSkinnyB<64, true, 5, 1>>(di, a, stream);
     else if (rows <= 64) return launch_skinny_b<sqb::CfgSkinnyB<64, false, 4, 2>>(di, a, stream);
-    else return launch_skinny_b<sqb::CfgSkinnyB<128, false, 3, 2>>(di, a, stream);
+    else return launch_skinny_b<sqb::CfgSkinnyB<128, false, 6, 1>>(di, a, stream);
 }
 
 sq_status product_args(sqb::ProductArgs &a, const void *X_8, const float *s_x, const int32_t *offsets, int64_t M, const void *W_8,
@@ -306,11 +306,12 @@ sq_status dispatch_impl(const int32_t *ids, int64_t T, int64_t k, int64_t E, int
     SQ_TRY(check_ptr(pos, T > 0, "pos"));
     DevInfo di;
     SQ_TRY(device_info(di));
-    const size_t smem = (static_cast<size_t>(sqm::DP_WARPS) * E + E + 1) * sizeof(int32_t);
+    const size_t smem = (static_cast<size_t>(sqm::DP_WARPS) * E + 2 * E + 1) * sizeof(int32_t);
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(sqm::DP_CTAS, T * k / sqm::DP_PAIRS));
     int per_sm = 0;
     SQ_TRY(kernel_setup(reinterpret_cast<const void *>(sqm::dispatch_kernel), 32 * sqm::DP_WARPS, smem, per_sm, "dispatch set-up"));
-    const cudaError_t e = launch_k(sqm::dispatch_kernel, dim3(1), dim3(32 * sqm::DP_WARPS), smem, stream, 0u, ids, T * k,
-                                   static_cast<int>(E), offsets, pos);
+    const cudaError_t e = launch_k(sqm::dispatch_kernel, dim3(static_cast<unsigned>(ctas)), dim3(32 * sqm::DP_WARPS), smem, stream,
+                                   static_cast<unsigned>(ctas), ids, T * k, static_cast<int>(E), offsets, pos);
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "dispatch launch");
 }
 

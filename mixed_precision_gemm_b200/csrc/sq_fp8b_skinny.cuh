@@ -156,6 +156,23 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         sqd::tmem_alloc(sqd::smem_u32(tmem_slot), C::TMEM);
         sqd::tmem_relinquish();
     }
+    // One matrix: which weights a CTA reads first does not depend on anything that the
+    // previous kernels write (weights come from sq_prepare_weights_fp8b, whose kernel
+    // lets none start before it has ended), so the first ring of them is fetched
+    // while those kernels finish.
+    const int b_lo = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
+    const int nblk = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S) - b_lo;
+    const int t0 = static_cast<int>(blockIdx.x) / S;
+    auto load_w = [&](int s, int b, int row) {
+        sqd::mbar_arrive_expect_tx(full(s), C::STAGE);
+#pragma unroll
+        for (int mat = 0; mat < MATS; ++mat)
+            sqd::tma_load_2d(stage(s) + mat * C::W_BYTES, &tm_w, full(s), b * BLK, row + mat * p.N);
+    };
+    const int chunks = static_cast<int>((p.M + MP - 1) / MP);
+    const int early = p.offsets || t0 >= chunks * p.nb ? 0 : min(NST, nblk);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < early; ++i) load_w(i, b_lo + i, t0 / chunks * 128);
     sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
     if (warp == 0) first_tiles(p, MP, lane, pre);
     sqd::tc_fence_before();
@@ -164,9 +181,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     const uint32_t tmem = *tmem_slot;
     const int tiles = pre[p.G];
     // Tiles t0, t0 + step, ..: a cluster has one at most (the host's grid covers them all then).
-    const int t0 = static_cast<int>(blockIdx.x) / S, step = S > 1 ? 0x40000000 : static_cast<int>(gridDim.x);
-    const int b_lo = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
-    const int nblk = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S) - b_lo;
+    const int step = S > 1 ? 0x40000000 : static_cast<int>(gridDim.x);
     SkinnyTile tile;
 
     if (warp == 0) {
@@ -179,12 +194,8 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             if (lane == 0) {
                 for (int i = 0; ok && i < nblk; ++i) {
                     if (!sqd::mbar_wait(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
-                    sqd::mbar_arrive_expect_tx(full(s), C::STAGE);
-                    const int x = (b_lo + i) * BLK;
-#pragma unroll
-                    for (int mat = 0; mat < MATS; ++mat)
-                        sqd::tma_load_2d(stage(s) + mat * C::W_BYTES, &tm_w, full(s), x, (tile.g * MATS + mat) * p.N + tile.tn * 128);
-                    sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), x, tile.m0);
+                    if (t != t0 || i >= early) load_w(s, b_lo + i, tile.g * MATS * p.N + tile.tn * 128);
+                    sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), (b_lo + i) * BLK, tile.m0);
                     last = s;
                     last_ph = ph;
                     if (++s == NST) { s = 0; ph ^= 1u; }

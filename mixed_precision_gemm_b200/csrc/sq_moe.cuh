@@ -273,25 +273,31 @@ __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteArgs a)
 // ---------------------------------------------------------------- dispatch
 // Order of the (token, choice) pairs by expert, stable: pos[i] = row of pair i
 // (its expert's offset plus the pairs of the same expert before it), -1 for an
-// index outside [0, E); offsets[E + 1].  One CTA: warp w owns a contiguous
-// range of pairs, counts its experts, and after a scan over warps and experts
-// gives out rows in order, 32 pairs at a time (lanes with the same expert rank
-// themselves by lane).  No atomics decide an order.
+// index outside [0, E); offsets[E + 1].  One cluster of up to 8 CTAs: every warp
+// owns a contiguous range of pairs and counts its experts; after sums over the
+// warps, the CTAs (their totals read through distributed shared memory) and the
+// experts, each gives out rows in order, 32 pairs at a time (lanes with the same
+// expert rank themselves by lane).  No atomics decide an order.
+// 32768 pairs of 64 experts: 31.5 us on one CTA, whose 32 warps share one SM's
+// matching and shared-memory atomics.
 constexpr int DP_WARPS = 32;
-constexpr int DP_UNROLL = 8;   // ids in flight per lane
+constexpr int DP_UNROLL = 8;      // ids in flight per lane
+constexpr int DP_CTAS = 8;
+constexpr int DP_PAIRS = 2048;    // pairs per CTA from which another CTA pays
 
 __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
                                                                  int32_t *__restrict__ offsets, int32_t *__restrict__ pos)
 {
-    extern __shared__ int32_t cnt[];   // [DP_WARPS][E], then [E + 1] offsets
-    int32_t *off = cnt + DP_WARPS * E;
+    extern __shared__ int32_t cnt[];   // [DP_WARPS][E], then [E + 1] offsets, then the CTA's [E] totals
+    int32_t *off = cnt + DP_WARPS * E, *tot = off + E + 1;
     sqd::pdl_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);   // one cluster
     for (int i = threadIdx.x; i < DP_WARPS * E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
     sqd::pdl_wait();
-    const int64_t per = ((pairs + DP_WARPS - 1) / DP_WARPS + 31) / 32 * 32;
-    const int64_t lo = min(per * w, pairs), hi = min(lo + per, pairs);
+    const int64_t per = ((pairs + DP_WARPS * ctas - 1) / (DP_WARPS * ctas) + 31) / 32 * 32;
+    const int64_t lo = min(per * (rank * DP_WARPS + w), pairs), hi = min(lo + per, pairs);
     int32_t *mine = cnt + w * E;
     for (int64_t i0 = lo; i0 < hi; i0 += 32 * DP_UNROLL) {
         int e[DP_UNROLL];
@@ -305,17 +311,41 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
             if (e[u] >= 0 && e[u] < E) atomicAdd(mine + e[u], 1);
     }
     __syncthreads();
-    // counts -> first row of every (warp, expert), relative to the expert
+    // counts -> first row of every (warp, expert), relative to the CTA's first of that expert
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int32_t s = 0;
+#pragma unroll 8
         for (int v = 0; v < DP_WARPS; ++v) {
             const int32_t c = cnt[v * E + e];
             cnt[v * E + e] = s;
             s += c;
         }
-        off[e + 1] = s;
+        tot[e] = s;
     }
-    __syncthreads();
+    if (ctas > 1) sqd::cluster_sync();   // every CTA's totals stand
+    else __syncthreads();
+    int32_t before[(MAX_EXPERTS + 32 * DP_WARPS - 1) / (32 * DP_WARPS)];   // of the CTAs before this one
+#pragma unroll
+    for (int q = 0; q < static_cast<int>(sizeof(before) / sizeof(int32_t)); ++q) {
+        const int e = threadIdx.x + q * 32 * DP_WARPS;
+        before[q] = 0;
+        if (e >= E) continue;
+        int32_t all = 0;
+        for (int c = 0; c < ctas; ++c) {
+            int32_t v;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(sqd::map_to_cta(sqd::smem_u32(tot + e), c)) : "memory");
+            if (c < rank) before[q] += v;
+            all += v;
+        }
+        off[e + 1] = all;
+    }
+    if (ctas > 1) sqd::cluster_sync();   // the totals are read: tot takes what comes before
+    else __syncthreads();
+#pragma unroll
+    for (int q = 0; q < static_cast<int>(sizeof(before) / sizeof(int32_t)); ++q) {
+        const int e = threadIdx.x + q * 32 * DP_WARPS;
+        if (e < E) tot[e] = before[q];
+    }
     if (w == 0) {   // inclusive scan of the experts' totals
         int32_t base = 0;
         if (lane == 0) off[0] = 0;
@@ -332,8 +362,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = off[e];
-    for (int e = lane; e < E; e += 32) mine[e] += off[e];
+    if (rank == 0)
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = off[e];
+    for (int e = lane; e < E; e += 32) mine[e] += off[e] + tot[e];
     __syncwarp();
     for (int64_t i0 = lo; i0 < hi; i0 += 32 * DP_UNROLL) {
         int e[DP_UNROLL];
