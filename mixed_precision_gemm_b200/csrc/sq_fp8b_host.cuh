@@ -128,6 +128,44 @@ sq_status launch_pair(const DevInfo &di, const sqb::ProductArgs &a, cudaStream_t
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block-scaled pair launch");
 }
 
+// Clusters of S CTAs that the device runs at once (asked once per kernel, size and
+// cluster; a GPC's SMs need not divide by S).
+struct ClusterFit {
+    const void *fn;
+    int dev;
+    size_t smem;
+    unsigned S;
+    int clusters;
+};
+std::vector<ClusterFit> g_fits;
+std::mutex g_fits_mu;
+
+sq_status cluster_fit(const void *fn, int threads, size_t smem, unsigned S, int &clusters)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lk(g_fits_mu);
+    for (const ClusterFit &f : g_fits)
+        if (f.fn == fn && f.dev == dev && f.smem == smem && f.S == S) {
+            clusters = f.clusters;
+            return SQ_OK;
+        }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg)) != cudaSuccess) return cuda_fail(e, "cluster occupancy");
+    g_fits.push_back({fn, dev, smem, S, clusters});
+    return SQ_OK;
+}
+
 // 128 weight rows x MP rows of X, K split over clusters.
 template <class C>
 sq_status launch_skinny_b(const DevInfo &di, const sqb::ProductArgs &a, cudaStream_t stream)
@@ -144,11 +182,16 @@ sq_status launch_skinny_b(const DevInfo &di, const sqb::ProductArgs &a, cudaStre
     auto kern = sqb::product_skinny_kernel<C>;
     int per_sm = 0;
     SQ_TRY(kernel_setup(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, smem, per_sm, "block-scaled skinny set-up"));
-    // Splits: as many as fill the SMs' places once, if every expert had one chunk, and
-    // leave a CTA two blocks.
+    // Splits: as many as let every tile run at once (experts counted with even shares of
+    // the rows), and leave a CTA two blocks.
     const int64_t places = static_cast<int64_t>(per_sm) * di.sms;
-    int64_t S = places / std::max<int64_t>(1, experts * a.nb);
-    S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(S, sqb::SB_MAX_SPLITS), a.kb / 2));
+    const int64_t at_once = a.offsets ? experts * ((a.M + experts * C::MP - 1) / (experts * C::MP)) * a.nb : tiles;
+    int64_t S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(places / at_once, sqb::SB_MAX_SPLITS), a.kb / 2));
+    for (; S > 1; --S) {
+        int fit = 0;
+        SQ_TRY(cluster_fit(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, smem, static_cast<unsigned>(S), fit));
+        if (fit >= at_once) break;
+    }
     const int64_t grid = S > 1 ? tiles * S : std::min(tiles, places);
     if (tiles > 0x3FFFFFFFll || grid > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld tiles", (long long)tiles);
     sqb::SkinnyBArgs sa;
@@ -167,11 +210,18 @@ sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
     // Rows per weight matrix, were they spread evenly (their counts are on the device).
     const int64_t rows = a.offsets ? (a.M + a.G - 1) / a.G : a.M;
     if (rows > 128) return launch_pair<SWIGLU>(di, a, stream);
-    if (rows <= 16) return launch_skinny_b<sqb::CfgSkinnyB<16, SWIGLU, SWIGLU ? 3 : 6, 2>>(di, a, stream);
-    if (rows <= 32) return launch_skinny_b<sqb::CfgSkinnyB<32, SWIGLU, SWIGLU ? 3 : 5, 2>>(di, a, stream);
-    if constexpr (SWIGLU) return launch_skinny_b<sqb::CfgSkinnyB<64, true, 5, 1>>(di, a, stream);
-    else if (rows <= 64) return launch_skinny_b<sqb::CfgSkinnyB<64, false, 4, 2>>(di, a, stream);
-    else return launch_skinny_b<sqb::CfgSkinnyB<128, false, 6, 1>>(di, a, stream);
+    // Rows of X per tile: all of them, or fewer where even every tile split as far as
+    // it goes leaves more than half of the SMs without a CTA (77 x 1000 x 1048: 9.4 us in
+    // tiles of 128 rows, 5.5 us in tiles of 32; with many tiles the larger ones are
+    // faster, 128 x 8192 x 8192: 29 us against 40 us in tiles of 64).
+    int mp = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || SWIGLU ? 64 : 128;
+    const int64_t most = std::min<int64_t>(sqb::SB_MAX_SPLITS, std::max(1, a.kb / 2)) * a.nb * (a.offsets ? std::min<int64_t>(a.G, a.M) : 1);
+    while (mp > 16 && 2 * most * ((rows + mp - 1) / mp) <= di.sms) mp /= 2;
+    if (mp == 16) return launch_skinny_b<sqb::CfgSkinnyB<16, SWIGLU, SWIGLU ? 3 : 6, 2>>(di, a, stream);
+    if (mp == 32) return launch_skinny_b<sqb::CfgSkinnyB<32, SWIGLU, SWIGLU ? 3 : 5, 2>>(di, a, stream);
+    if constexpr (SWIGLU) return launch_skinny_b<sqb::CfgSkinnyB<64, true, 4, 1>>(di, a, stream);
+    else if (mp == 64) return launch_skinny_b<sqb::CfgSkinnyB<64, false, 4, 2>>(di, a, stream);
+    else return launch_skinny_b<sqb::CfgSkinnyB<128, false, 4, 1>>(di, a, stream);
 }
 
 sq_status product_args(sqb::ProductArgs &a, const void *X_8, const float *s_x, const int32_t *offsets, int64_t M, const void *W_8,

@@ -5,9 +5,12 @@
 // of scale blocks; SwiGLU: 128 gate rows and the same 128 up rows) by MP rows of
 // X, as D^T = W X^T: the weight rows are the MMA's M side (TMEM lanes) and the MP
 // rows of X its N side, so that few rows cost little.  Each 128-channel block of
-// D^T goes to a small ring of TMEM buffers; four epilogue warps (a thread per
-// weight row) add it, times sx[m,b] sw[b], to MP sums in registers.  sx sw of four
-// blocks at a time is a table in shared memory, read as broadcasts.
+// D^T goes to the TMEM buffer of its ring stage; four epilogue warps (a thread per
+// weight row) add it, times sx[m,b] sw[b], to MP sums in registers and give the
+// stage, operands and buffer, back to the loads.  So the issuing thread has one
+// wait and one commit per block: with a wait and a commit of its own for the
+// buffers a block took it some 980 cycles, of which the MMAs are 512.  sx sw of
+// four blocks at a time is a table in shared memory, read as broadcasts.
 //
 // With enough tiles for every SM the kernel is persistent (S = 1): each CTA takes
 // every gridDim.x-th tile, its loads running ahead into the next tile while the
@@ -42,19 +45,18 @@ struct CfgSkinnyB {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int STAGE = MATS * W_BYTES + MP * 128;
     static constexpr int COLS = MATS * MP;                       // TMEM columns per block
-    static constexpr int NB = 256 / COLS < 4 ? 256 / COLS : 4;   // TMEM buffers
-    static constexpr int TMEM = NB * COLS <= 32 ? 32 : NB * COLS <= 64 ? 64 : NB * COLS <= 128 ? 128 : 256;
+    static constexpr int TMEM = NST * COLS <= 32 ? 32 : NST * COLS <= 64 ? 64 : NST * COLS <= 128 ? 128 : NST * COLS <= 256 ? 256 : 512;
     static constexpr int OFF_TAB = NST * STAGE;                  // [2][4][MATS][MP] products of scales
     static constexpr int OFF_MAX = OFF_TAB + 2 * 4 * MATS * MP * 4;   // SwiGLU: [4 warps][MP] maxima, [3][MP] scale constants
     static constexpr int OFF_BAR = OFF_MAX + (SWIGLU ? 7 * MP * 4 : 0);
-    static constexpr int NBAR = 2 * NST + 2 * NB + 1;
+    static constexpr int NBAR = 3 * NST + 1;                     // full[NST] done[NST] empty[NST] drain
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;          // TMEM address, abort flag
     static constexpr int OFF_PRE = OFF_MISC + 8;                 // first tile of each expert
     static constexpr int smem(int G) { return OFF_PRE + 4 * (G + 1) + 768; }
     static_assert(STAGE % 1024 == 0, "swizzled tiles");
     static_assert(MATS * (MP / 4 + SB_MAX_SPLITS - 1) * 2048 <= NST * STAGE, "the exchanged sums fit in the ring");
     static_assert(smem(512) <= 232448, "shared memory");
-    static_assert((smem(256) + 1024) * PER_SM <= 233472 && TMEM * PER_SM <= 512, "an SM's share");
+    static_assert((smem(256) + 1024) * PER_SM <= 233472 && NST * COLS <= TMEM && TMEM * PER_SM <= 512, "an SM's share");
 };
 
 struct SkinnyBArgs {
@@ -114,7 +116,7 @@ template <class C>
 __global__ void __launch_bounds__(SB_THREADS, C::PER_SM)
 product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const SkinnyBArgs args)
 {
-    constexpr int MP = C::MP, NST = C::NST, NB = C::NB, MATS = C::MATS;
+    constexpr int MP = C::MP, NST = C::NST, MATS = C::MATS;
     constexpr bool SWIGLU = C::SWIGLU;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -127,10 +129,9 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
 
     const uint32_t bar0 = sbase + C::OFF_BAR;
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (NST + s); };
-    auto bfull = [&](int j) { return bar0 + 8u * (2 * NST + j); };
-    auto bempty = [&](int j) { return bar0 + 8u * (2 * NST + NB + j); };
-    const uint32_t drain = bar0 + 8u * (2 * NST + 2 * NB);
+    auto done = [&](int s) { return bar0 + 8u * (NST + s); };
+    auto empty = [&](int s) { return bar0 + 8u * (2 * NST + s); };
+    const uint32_t drain = bar0 + 8u * (3 * NST);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC + 4);
     int32_t *pre = reinterpret_cast<int32_t *>(smem + C::OFF_PRE);
@@ -138,12 +139,9 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            sqd::mbar_init(full(s), 1);
-            sqd::mbar_init(empty(s), 1);
-        }
-        for (int j = 0; j < NB; ++j) {
-            sqd::mbar_init(bfull(j), 1);
-            sqd::mbar_init(bempty(j), 4);
+            sqd::mbar_init(full(s), 1);    // loads
+            sqd::mbar_init(done(s), 1);    // MMAs
+            sqd::mbar_init(empty(s), 4);   // epilogue warps
         }
         sqd::mbar_init(drain, 1);
         *abort_flag = 0u;
@@ -208,25 +206,22 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
             constexpr uint32_t idesc = sqd::make_idesc_e4m3(128, MP);
-            int s = 0, j = 0;
-            uint32_t ph = 0, bph = 0;
+            const uint64_t desc0 = sqd::make_sw128_desc(stage(0));   // (the ring ends below the address field's 256 KB)
+            int s = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int t = t0; ok && t < tiles; t += step) {
                 for (int i = 0; i < nblk; ++i) {
-                    const uint64_t ad = sqd::make_sw128_desc(stage(s));
-                    const uint64_t bd = sqd::make_sw128_desc(stage(s) + MATS * C::W_BYTES);
-                    if (!sqd::mbar_wait(full(s), ph, abort_flag, SITE_SB_MMA) ||
-                        !sqd::mbar_wait(bempty(j), bph ^ 1u, abort_flag, SITE_SB_MMA)) { ok = false; break; }
+                    const uint64_t ad = desc0 + static_cast<uint64_t>(s * (C::STAGE >> 4)), bd = ad + (MATS * C::W_BYTES >> 4);
+                    if (!sqd::mbar_wait(full(s), ph, abort_flag, SITE_SB_MMA)) { ok = false; break; }
                     sqd::tc_fence_after();
 #pragma unroll
                     for (int mat = 0; mat < MATS; ++mat)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            sqd::mma_f8(tmem + j * C::COLS + mat * MP, ad + mat * (C::W_BYTES >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                    sqd::mma_commit(bfull(j));
-                    sqd::mma_commit(empty(s));
+                            sqd::mma_f8(tmem + s * C::COLS + mat * MP, ad + mat * (C::W_BYTES >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                    sqd::mma_commit(done(s));
                     if (++s == NST) { s = 0; ph ^= 1u; }
-                    if (++j == NB) { j = 0; bph ^= 1u; }
                 }
             }
             if (!ok) {
@@ -245,8 +240,8 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         float *wmax = reinterpret_cast<float *>(smem + C::OFF_MAX);
         const int sw_up = p.nb * p.s_ld / 4;    // the up matrix's scales behind the gate's
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        int j = 0, group = 0;
-        uint32_t bph = 0;
+        int st = 0, group = 0;
+        uint32_t ph = 0;
         for (int t = t0; t < tiles; t += step) {
             tile.seek(p, MP, pre, t, lane);
             const bool row_ok = et < MP && tile.m0 + et < tile.m_end;
@@ -281,18 +276,18 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     if (((q + 1) << 2) < b_lo + nblk) fetch(q + 1);
                 }
-                sqd::mbar_wait(bfull(j), bph, abort_flag, SITE_SB_EPI);
+                sqd::mbar_wait(done(st), ph, abort_flag, SITE_SB_EPI);
                 sqd::tc_fence_after();
                 const float4 *tb = reinterpret_cast<const float4 *>(tq + (b & 3) * MATS * MP);
 #pragma unroll
                 for (int ch = 0; ch < C::COLS / 16; ++ch) {
                     uint32_t v[16];
-                    sqd::tmem_ld_32x32b_x16(tl + j * C::COLS + 16 * ch, v);
+                    sqd::tmem_ld_32x32b_x16(tl + st * C::COLS + 16 * ch, v);
                     sqd::tmem_wait_ld_dep1(v);
                     if (ch + 1 == C::COLS / 16) {
                         sqd::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) sqd::mbar_arrive(bempty(j));
+                        if (lane == 0) sqd::mbar_arrive(empty(st));
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -302,7 +297,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                         a1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), make_float2(s.z, s.w), a1);
                     }
                 }
-                if (++j == NB) { j = 0; bph ^= 1u; }
+                if (++st == NST) { st = 0; ph ^= 1u; }
             }
             const int n = tile.tn * 128 + wr;
             const int64_t m0 = tile.m0;
