@@ -35,7 +35,7 @@ __device__ __forceinline__ BlockScale block_scale(float amax)
 {
     BlockScale b;
     b.zero = amax == 0.0f;
-    b.s = b.zero ? 0.0f : __fdiv_rn(amax, kTop);
+    b.s = sqq::row_scale(amax, kTop, 1.0f / kTop);   // (0 for 0)
     b.up = !b.zero && b.s < sqq::kTinyScale;
     const float s1 = b.up ? b.s * sqq::kUpScale : b.s;
     const float inv = b.zero ? 0.0f : __frcp_rn(s1);
@@ -63,48 +63,49 @@ __device__ __forceinline__ uint32_t absmax8(const uint4 &v)
 }
 
 constexpr int QB_THREADS = 256;
-constexpr int QB_CHUNKS = 4;                     // 8-channel chunks per lane
-constexpr int QB_SEG = 32 * QB_CHUNKS * 8;       // channels per warp task
 
-// Codes and scales of the rows of X.  One warp takes 1024 channels of a row:
+// Codes and scales of the rows of X.  One warp takes 256 CHUNKS channels of a row:
 // lane l holds chunks l, l + 32, ... of 8 channels (16 bytes), so 16 lanes
 // share a block of 128 and its maximum takes four shuffles.
 // With pos (top > 0) row t of X goes to the `top` rows pos[t * top + j] of the
 // outputs (entries outside [0, rows_out) are skipped): one read of a token for all
-// of its experts' copies; a token without any is not read.
+// of its experts' copies; a token without any is not read.  With few tokens
+// (gridDim.y = top) a warp writes one copy only.
 // Memory-bound: 2 K bytes read and (K + 4 K / 128) written per output row.
+template <int CHUNKS>
 __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__restrict__ X, int64_t rows, int K, int64_t ldx,
                                                            int k_pad, int s_ld, const int32_t *__restrict__ pos, int top,
                                                            int64_t rows_out, uint8_t *__restrict__ X_8,
                                                            float *__restrict__ s_x)
 {
+    constexpr int SEG = 32 * CHUNKS * 8;
     sqd::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int segs = (s_ld * BLK + QB_SEG - 1) / QB_SEG;
+    const int segs = (s_ld * BLK + SEG - 1) / SEG;
     const int64_t tasks = rows * segs;
     const int64_t wpg = static_cast<int64_t>(gridDim.x) * (QB_THREADS / 32);
+    const int j_lo = gridDim.y > 1 ? blockIdx.y : 0, j_hi = gridDim.y > 1 ? j_lo + 1 : max(top, 1);
     sqd::pdl_wait();
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * (QB_THREADS / 32) + (threadIdx.x >> 5); w < tasks; w += wpg) {
         const int64_t r = w / segs;
-        const int c0 = static_cast<int>(w - r * segs) * (QB_SEG / 8) + lane;
+        const int c0 = static_cast<int>(w - r * segs) * (SEG / 8) + lane;
         int32_t dst = -1;                       // lane j: the row's j-th copy
         if (top > 0) {
-            if (lane < top) dst = pos[r * top + lane];
+            if (lane >= j_lo && lane < j_hi) dst = pos[r * top + lane];
             if (dst >= rows_out) dst = -1;
             if (!__any_sync(0xFFFFFFFFu, dst >= 0)) continue;
         }
         const uint16_t *row = X + r * ldx;
-        uint4 v[QB_CHUNKS];
-        uint2 q[QB_CHUNKS];
-        float sc[QB_CHUNKS];
+        uint4 v[CHUNKS];
+        uint2 q[CHUNKS];
+        float sc[CHUNKS];
 #pragma unroll
-        for (int i = 0; i < QB_CHUNKS; ++i) {
+        for (int i = 0; i < CHUNKS; ++i) {
             const int c = c0 + 32 * i;
             v[i] = c < (K >> 3) ? sqd::ld_nc_v4(row + 8 * c) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < QB_CHUNKS; ++i) {
-            const int c = c0 + 32 * i;
+        for (int i = 0; i < CHUNKS; ++i) {
             uint32_t m = absmax8(v[i]);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -112,11 +113,11 @@ __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__res
             q[i] = block_codes(v[i], b);
             sc[i] = b.s;
         }
-        for (int j = 0; j < (top > 0 ? top : 1); ++j) {
+        for (int j = j_lo; j < j_hi; ++j) {
             const int64_t d = top > 0 ? __shfl_sync(0xFFFFFFFFu, dst, j) : r;
             if (d < 0) continue;
 #pragma unroll
-            for (int i = 0; i < QB_CHUNKS; ++i) {
+            for (int i = 0; i < CHUNKS; ++i) {
                 const int c = c0 + 32 * i;
                 if (8 * c < k_pad) *reinterpret_cast<uint2 *>(X_8 + d * k_pad + 8 * c) = q[i];
                 if ((lane & 15) == 0 && (c >> 4) < s_ld) s_x[d * s_ld + (c >> 4)] = sc[i];

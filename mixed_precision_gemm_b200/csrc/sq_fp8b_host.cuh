@@ -89,10 +89,14 @@ sq_status quant_fp8b_impl(const void *X, int64_t M, int64_t K, int64_t ldx, cons
     SQ_TRY(check_ptr(s_x, true, "s_x"));
     DevInfo di;
     SQ_TRY(device_info(di));
-    const int64_t tasks = M * ((fp8b_s_ld(K) * 128 + sqb::QB_SEG - 1) / sqb::QB_SEG);
+    // 1024 channels per warp; with a few warps' worth of them 256, and one copy of a row per
+    // warp (8 copies of one token of 4096 channels: 5.8 us and 4.1 us).
+    const bool few = M * ((fp8b_s_ld(K) + 7) / 8) <= 64;
+    const int64_t tasks = M * ((fp8b_s_ld(K) * 128 + (few ? 255 : 1023)) / (few ? 256 : 1024));
     const int64_t blocks = std::min<int64_t>((tasks + sqb::QB_THREADS / 32 - 1) / (sqb::QB_THREADS / 32), 8ll * di.sms);
-    const cudaError_t e = launch_k(sqb::quant_kernel, dim3(static_cast<unsigned>(blocks)), dim3(sqb::QB_THREADS), 0, stream, 0u,
-                                   static_cast<const uint16_t *>(X), M, static_cast<int>(K), ldx,
+    const cudaError_t e = launch_k(few ? sqb::quant_kernel<1> : sqb::quant_kernel<4>,
+                                   dim3(static_cast<unsigned>(blocks), few ? static_cast<unsigned>(std::max<int64_t>(1, top)) : 1u),
+                                   dim3(sqb::QB_THREADS), 0, stream, 0u, static_cast<const uint16_t *>(X), M, static_cast<int>(K), ldx,
                                    static_cast<int>(fp8b_k_pad(K)), static_cast<int>(fp8b_s_ld(K)), pos, static_cast<int>(top),
                                    rows_out, static_cast<uint8_t *>(X_8), s_x);
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "block quantizer launch");

@@ -457,3 +457,19 @@ def test_captured_and_on_other_streams(T):
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(y, want[2])
     sq.sq_check()
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1048), (7, 1000, 264), (16, 8192, 520), (16, 136, 128), (3, 8, 8)])
+def test_linear_is_its_two_steps(M, K, N):
+    """Few rows are quantized inside the product: the same codes, scales and order of sums."""
+    x, w = activations(M, K), weights(N, K)
+    x[0, : min(128, K)] = 0
+    x[-1, : min(8, K)] *= 2.0 ** -125
+    pw = sq.prepare_weights_fp8b(w)
+    xc, xs = sq.quant_fp8b(x)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    sq.sq_gemm_fp8b(xc, xs, pw.W_8, pw.s_w, M, N, K, y)
+    assert torch.equal(sq.linear_fp8b(x, pw), y)
+    wide = torch.zeros(M, K + 16, dtype=torch.bfloat16, device=DEV)
+    wide[:, 8:K + 8] = x
+    assert torch.equal(sq.linear_fp8b(wide[:, 8:K + 8], pw), y)
