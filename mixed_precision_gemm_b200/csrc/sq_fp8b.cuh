@@ -194,23 +194,50 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int g, int64_t
     hi = min(max(static_cast<int64_t>(a.offsets[g + 1]), lo), a.M);
 }
 
-// silu(g) u with the hardware's exponential and reciprocal (about 2^-21 of the
-// value, far below the 2^-12 that a product's sum is known to): one MUFU each where
-// expf and an exact quotient cost some 30 instructions.  e^-g = inf gives 0.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// E4M3 codes of two fp32 values over a block's scale (rounded quotients as in
-// sq_rowquant.cuh), in the low 16 bits.
-__device__ __forceinline__ uint32_t codes2(float x, float y, const BlockScale &b)
+// silu(g) u of two columns with the hardware's exponential and reciprocal (about 2^-21
+// of the value, far below the 2^-12 that a product's sum is known to): one MUFU
+// each where expf and an exact quotient cost some 30 instructions, the rest packed.
+// e^-g = inf gives g * 0 * u = 0.
+__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u)
 {
-    if (b.zero) return 0u;
-    uint64_t v = sqq::f2_pack(__float_as_uint(x), __float_as_uint(y));
-    if (b.up) v = sqq::f2_mul(v, b.rs.up2);
-    const uint64_t q0 = sqq::f2_mul(v, b.rs.inv2);
-    const uint64_t q1 = sqq::f2_fma(sqq::f2_fma(q0, b.rs.negs2, v), b.rs.inv2, q0);
-    uint32_t t0, t1;
-    sqq::f2_unpack(q1, t0, t1);
-    return __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(t0), __uint_as_float(t1)), __NV_SATFINITE, __NV_E4M3);
+    const float2 t = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return __fmul2_rn(__fmul2_rn(g, r), u);
+}
+
+// A block's scale and what its codes need: the scale's inverse and negative, of a
+// scale brought up by 2^64 if it is tiny (the values have to be, too).  A zero
+// block's constants take zeros of either sign to code 0.
+struct CodeScale {
+    float s, inv, neg, up;
+};
+
+__device__ __forceinline__ CodeScale code_scale(float amax)
+{
+    const BlockScale b = block_scale(amax);
+    CodeScale c;
+    uint32_t inv, neg, hi;
+    sqq::f2_unpack(b.rs.inv2, inv, hi);
+    sqq::f2_unpack(b.rs.negs2, neg, hi);
+    c.s = b.s;
+    c.inv = b.zero ? 1.0f : __uint_as_float(inv);
+    c.neg = b.zero ? -1.0f : __uint_as_float(neg);
+    c.up = b.up ? sqq::kUpScale : 1.0f;
+    return c;
+}
+
+// E4M3 codes of two (brought up) fp32 values, in the low 16 bits: the rounded
+// quotients as in sq_rowquant.cuh.
+__device__ __forceinline__ uint32_t codes2(float2 v, float2 inv, float2 neg)
+{
+    const float2 q0 = __fmul2_rn(v, inv);
+    const float2 q1 = __ffma2_rn(__ffma2_rn(q0, neg, v), inv, q0);
+    return __nv_cvt_float2_to_fp8x2(q1, __NV_SATFINITE, __NV_E4M3);
 }
 
 }  // namespace sqb

@@ -337,34 +337,42 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                     const uint4 o = sqd::lds128(box + i * 512 + lane * 16);
                     const float oth[4] = {__uint_as_float(o.x), __uint_as_float(o.y), __uint_as_float(o.z), __uint_as_float(o.w)};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float own = half ? acc[64 + 4 * i + j] : acc[4 * i + j];
-                        const float gt = half ? oth[j] : own, upv = half ? own : oth[j];
-                        const float hv = n0 + 4 * i + j < p.N ? silu_mul(gt, upv) : 0.0f;
-                        acc[4 * i + j] = hv;   // (the columns ..63 are used up)
-                        mx = fmaxf(mx, fabsf(hv));
+                    for (int j = 0; j < 4; j += 2) {
+                        const float2 own = half ? make_float2(acc[64 + 4 * i + j], acc[64 + 4 * i + j + 1])
+                                                : make_float2(acc[4 * i + j], acc[4 * i + j + 1]);
+                        const float2 got = make_float2(oth[j], oth[j + 1]);
+                        float2 h = silu_mul2(half ? got : own, half ? own : got);
+                        if (n0 + 4 * i + j >= p.N) h = make_float2(0.0f, 0.0f);   // (N is even)
+                        acc[4 * i + j] = h.x;          // (the columns ..63 are used up)
+                        acc[4 * i + j + 1] = h.y;
+                        mx = fmaxf(mx, fmaxf(fabsf(h.x), fabsf(h.y)));
                     }
                 }
                 __syncwarp();   // this warp has read its box: its rows' maxima go there
                 sqd::sts32(box + 4 * lane, __float_as_uint(mx));
                 if (!meet()) break;
                 mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
-                const BlockScale bs = block_scale(mx);
+                const CodeScale cs = code_scale(mx);
+                if (cs.up != 1.0f) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) acc[i] *= cs.up;
+                }
                 const int64_t m = c_row0 + lane;
                 if (m < c_end) {
                     uint8_t *out = p.H_8 + m * p.h_pad + n0;
+                    const float2 inv = make_float2(cs.inv, cs.inv), neg = make_float2(cs.neg, cs.neg);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float *h = acc + 16 * i + 4 * j;
-                            w[j] = codes2(h[0], h[1], bs) | (codes2(h[2], h[3], bs) << 16);
+                            w[j] = codes2(make_float2(h[0], h[1]), inv, neg) | (codes2(make_float2(h[2], h[3]), inv, neg) << 16);
                         }
                         *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (half == 0) {
-                        p.s_h[m * p.h_ld + c_tni] = bs.s;
+                        p.s_h[m * p.h_ld + c_tni] = cs.s;
                         if (c_tni == p.nb - 1)
                             for (int z = p.nb; z < p.h_ld; ++z) p.s_h[m * p.h_ld + z] = 0.0f;
                     }

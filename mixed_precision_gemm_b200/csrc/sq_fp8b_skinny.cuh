@@ -319,7 +319,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
 #pragma unroll
                     for (int c = 0; c < MP / 2; ++c) {
                         const float2 gt = acc[0][c], up = acc[MATS - 1][c];
-                        const float2 h = n < p.N ? make_float2(silu_mul(gt.x, up.x), silu_mul(gt.y, up.y)) : make_float2(0.0f, 0.0f);
+                        const float2 h = n < p.N ? silu_mul2(gt, up) : make_float2(0.0f, 0.0f);
                         acc[0][c] = h;
                         const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h.x)));
                         const uint32_t my = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h.y)));
@@ -328,15 +328,12 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     float *consts = wmax + 4 * MP;   // of each row's scale: its inverse, its negative, the factor of tiny ones
                     if (et < MP) {
-                        const BlockScale bs = block_scale(fmaxf(fmaxf(wmax[et], wmax[MP + et]), fmaxf(wmax[2 * MP + et], wmax[3 * MP + et])));
-                        uint32_t inv, neg, hi;
-                        sqq::f2_unpack(bs.rs.inv2, inv, hi);
-                        sqq::f2_unpack(bs.rs.negs2, neg, hi);
-                        consts[et] = bs.zero ? 1.0f : __uint_as_float(inv);    // (1: zeros of either sign to code 0)
-                        consts[MP + et] = bs.zero ? -1.0f : __uint_as_float(neg);
-                        consts[2 * MP + et] = bs.up ? sqq::kUpScale : 1.0f;
+                        const CodeScale cs = code_scale(fmaxf(fmaxf(wmax[et], wmax[MP + et]), fmaxf(wmax[2 * MP + et], wmax[3 * MP + et])));
+                        consts[et] = cs.inv;
+                        consts[MP + et] = cs.neg;
+                        consts[2 * MP + et] = cs.up;
                         if (et < rows) {
-                            p.s_h[(m0 + et) * p.h_ld + tile.tn] = bs.s;
+                            p.s_h[(m0 + et) * p.h_ld + tile.tn] = cs.s;
                             if (tile.tn == p.nb - 1)
                                 for (int q = p.nb; q < p.h_ld; ++q) p.s_h[(m0 + et) * p.h_ld + q] = 0.0f;
                         }
@@ -350,9 +347,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                             const float2 h = acc[0][c / 2 + k], inv = *reinterpret_cast<const float2 *>(consts + c + 2 * k);
                             const float2 neg = *reinterpret_cast<const float2 *>(consts + MP + c + 2 * k);
                             const float2 v = __fmul2_rn(h, *reinterpret_cast<const float2 *>(consts + 2 * MP + c + 2 * k));
-                            const float2 q0 = __fmul2_rn(v, inv);
-                            const float2 q1 = __ffma2_rn(__ffma2_rn(q0, neg, v), inv, q0);
-                            w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q1, __NV_SATFINITE, __NV_E4M3)) << (16 * k);
+                            w |= codes2(v, inv, neg) << (16 * k);
                         }
                         w = transpose_bytes(w, lane);
                         const int r = c + (lane & 3);
@@ -405,8 +400,9 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     } else {
                         const bool in = nn < p.N;
                         const float4 gt = sum[0], up = sum[MATS - 1];
-                        const float h[4] = {in ? silu_mul(gt.x, up.x) : 0.0f, in ? silu_mul(gt.y, up.y) : 0.0f,
-                                            in ? silu_mul(gt.z, up.z) : 0.0f, in ? silu_mul(gt.w, up.w) : 0.0f};
+                        const float2 h01 = silu_mul2(make_float2(gt.x, gt.y), make_float2(up.x, up.y));
+                        const float2 h23 = silu_mul2(make_float2(gt.z, gt.w), make_float2(up.z, up.w));
+                        const float h[4] = {in ? h01.x : 0.0f, in ? h01.y : 0.0f, in ? h23.x : 0.0f, in ? h23.y : 0.0f};
                         red[f * 128 + et] = make_float4(h[0], h[1], h[2], h[3]);   // (source 0's gate sums are used up)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -419,11 +415,13 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     const float *hs = reinterpret_cast<const float *>(smem);   // [four][column][row of the four]
                     for (int r = et >> 5; r < mine; r += 4) {       // a warp per row, four columns per lane
-                        const BlockScale bs = block_scale(fmaxf(fmaxf(wmax[r], wmax[MP + r]), fmaxf(wmax[2 * MP + r], wmax[3 * MP + r])));
+                        const CodeScale cs = code_scale(fmaxf(fmaxf(wmax[r], wmax[MP + r]), fmaxf(wmax[2 * MP + r], wmax[3 * MP + r])));
                         const float *h = hs + ((r >> 2) * 128 + 4 * lane) * 4 + (r & 3);
+                        const float2 inv = make_float2(cs.inv, cs.inv), neg = make_float2(cs.neg, cs.neg);
                         *reinterpret_cast<uint32_t *>(p.H_8 + (m0 + r0 + r) * p.h_pad + tile.tn * 128 + 4 * lane) =
-                            codes2(h[0], h[4], bs) | (codes2(h[8], h[12], bs) << 16);
-                        if (lane == 0) p.s_h[(m0 + r0 + r) * p.h_ld + tile.tn] = bs.s;
+                            codes2(make_float2(h[0] * cs.up, h[4] * cs.up), inv, neg) |
+                            (codes2(make_float2(h[8] * cs.up, h[12] * cs.up), inv, neg) << 16);
+                        if (lane == 0) p.s_h[(m0 + r0 + r) * p.h_ld + tile.tn] = cs.s;
                         if (tile.tn == p.nb - 1 && p.nb + lane < p.h_ld) p.s_h[(m0 + r0 + r) * p.h_ld + p.nb + lane] = 0.0f;
                     }
                 }
