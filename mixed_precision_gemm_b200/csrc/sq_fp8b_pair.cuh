@@ -37,6 +37,8 @@
 // never leaves the SM in another form.
 #pragma once
 
+#include <type_traits>
+
 #include "sq_fp8b.cuh"
 #include "sq_gemm_common.cuh"
 
@@ -320,63 +322,70 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
             if constexpr (SWIGLU) {
                 // Gate and up warp of the same rows exchange halves: the gate warp hands over its
                 // columns 64.., the up warp its columns ..63; then 64 columns of both are here.
-                const uint32_t partner = sbase + PP_OFF_BOX + ((warp - PP_EPI0) ^ 4) * PP_BOX;
+                // (one copy of the code per half: selects between the halves of acc would
+                // cost four instructions per column)
+                const auto finish = [&](auto up_warp) -> bool {
+                    constexpr int OWN = up_warp.value ? 64 : 0, GIVE = 64 - OWN;
+                    const uint32_t partner = sbase + PP_OFF_BOX + ((warp - PP_EPI0) ^ 4) * PP_BOX;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    // (selects, not an indexed array: acc has to stay in registers)
-                    uint32_t o[4];
+                    for (int i = 0; i < 16; ++i)
+                        sqd::sts128(partner + i * 512 + lane * 16, __float_as_uint(acc[GIVE + 4 * i]), __float_as_uint(acc[GIVE + 4 * i + 1]),
+                                    __float_as_uint(acc[GIVE + 4 * i + 2]), __float_as_uint(acc[GIVE + 4 * i + 3]));
+                    if (!meet()) return false;
+                    const int n0 = c_tni * 128 + OWN;
+                    float mx = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(half ? acc[4 * i + j] : acc[64 + 4 * i + j]);
-                    sqd::sts128(partner + i * 512 + lane * 16, o[0], o[1], o[2], o[3]);
-                }
-                if (!meet()) break;
-                float mx = 0.0f;
-                const int n0 = c_tni * 128 + half * 64;
+                    for (int i = 0; i < 16; ++i) {
+                        const uint4 o = sqd::lds128(box + i * 512 + lane * 16);
+                        const float2 got[2] = {make_float2(__uint_as_float(o.x), __uint_as_float(o.y)),
+                                               make_float2(__uint_as_float(o.z), __uint_as_float(o.w))};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint4 o = sqd::lds128(box + i * 512 + lane * 16);
-                    const float oth[4] = {__uint_as_float(o.x), __uint_as_float(o.y), __uint_as_float(o.z), __uint_as_float(o.w)};
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        const float2 own = half ? make_float2(acc[64 + 4 * i + j], acc[64 + 4 * i + j + 1])
-                                                : make_float2(acc[4 * i + j], acc[4 * i + j + 1]);
-                        const float2 got = make_float2(oth[j], oth[j + 1]);
-                        float2 h = silu_mul2(half ? got : own, half ? own : got);
-                        if (n0 + 4 * i + j >= p.N) h = make_float2(0.0f, 0.0f);   // (N is even)
-                        acc[4 * i + j] = h.x;          // (the columns ..63 are used up)
-                        acc[4 * i + j + 1] = h.y;
-                        mx = fmaxf(mx, fmaxf(fabsf(h.x), fabsf(h.y)));
-                    }
-                }
-                __syncwarp();   // this warp has read its box: its rows' maxima go there
-                sqd::sts32(box + 4 * lane, __float_as_uint(mx));
-                if (!meet()) break;
-                mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
-                const CodeScale cs = code_scale(mx);
-                if (cs.up != 1.0f) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) acc[i] *= cs.up;
-                }
-                const int64_t m = c_row0 + lane;
-                if (m < c_end) {
-                    uint8_t *out = p.H_8 + m * p.h_pad + n0;
-                    const float2 inv = make_float2(cs.inv, cs.inv), neg = make_float2(cs.neg, cs.neg);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float *h = acc + 16 * i + 4 * j;
-                            w[j] = codes2(make_float2(h[0], h[1]), inv, neg) | (codes2(make_float2(h[2], h[3]), inv, neg) << 16);
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 own = make_float2(acc[OWN + 4 * i + 2 * j], acc[OWN + 4 * i + 2 * j + 1]);
+                            const float2 h = up_warp.value ? silu_mul2(got[j], own) : silu_mul2(own, got[j]);
+                            acc[OWN + 4 * i + 2 * j] = h.x;
+                            acc[OWN + 4 * i + 2 * j + 1] = h.y;
                         }
-                        *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (half == 0) {
-                        p.s_h[m * p.h_ld + c_tni] = cs.s;
-                        if (c_tni == p.nb - 1)
-                            for (int z = p.nb; z < p.h_ld; ++z) p.s_h[m * p.h_ld + z] = 0.0f;
+                    if (n0 + 64 > p.N) {                 // the last tile: columns past N
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (n0 + i >= p.N) acc[OWN + i] = 0.0f;
                     }
-                }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) mx = fmaxf(mx, fabsf(acc[OWN + i]));
+                    __syncwarp();   // this warp has read its box: its rows' maxima go there
+                    sqd::sts32(box + 4 * lane, __float_as_uint(mx));
+                    if (!meet()) return false;
+                    mx = fmaxf(mx, __uint_as_float(sqd::lds32(partner + 4 * lane)));
+                    const CodeScale cs = code_scale(mx);
+                    if (cs.up != 1.0f) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) acc[OWN + i] *= cs.up;
+                    }
+                    const int64_t m = c_row0 + lane;
+                    if (m < c_end) {
+                        uint8_t *out = p.H_8 + m * p.h_pad + n0;
+                        const float2 inv = make_float2(cs.inv, cs.inv), neg = make_float2(cs.neg, cs.neg);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float *h = acc + OWN + 16 * i + 4 * j;
+                                w[j] = codes2(make_float2(h[0], h[1]), inv, neg) | (codes2(make_float2(h[2], h[3]), inv, neg) << 16);
+                            }
+                            *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        if (!up_warp.value) {
+                            p.s_h[m * p.h_ld + c_tni] = cs.s;
+                            if (c_tni == p.nb - 1)
+                                for (int z = p.nb; z < p.h_ld; ++z) p.s_h[m * p.h_ld + z] = 0.0f;
+                        }
+                    }
+                    return true;
+                };
+                if (!(half ? finish(std::true_type()) : finish(std::false_type()))) break;
             } else {
                 const int n0 = c_tni * PP_BN + half * PP_COLS;
                 // the previous tile's bulk stores have read the boxes
