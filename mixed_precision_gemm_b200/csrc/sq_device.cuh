@@ -93,6 +93,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
 }
 
+// The same for waits that are mostly a few hundred cycles long: the clock, which
+// a waiting thread would read first thing, is left alone for the first 64 tries.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, unsigned site)
+{
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag, site);
+}
+
 // Wait used only on the way out of an aborted CTA: lets copies and MMAs that
 // are still in flight land before the CTA releases its memory.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)

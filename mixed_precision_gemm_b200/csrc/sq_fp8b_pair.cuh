@@ -105,6 +105,28 @@ struct PairArgs {
     int nt, group_m;
 };
 
+// A block's sums, times the scale sv, added to the tile's; the TMEM buffer goes back
+// to the MMAs (barrier `release`) once it is read.
+__device__ __forceinline__ void add_block(float2 (&sums)[PP_COLS / 2], uint32_t src, float sv, int lane, uint32_t release)
+{
+    sqd::tc_fence_after();
+    const float2 s2 = make_float2(sv, sv);
+#pragma unroll
+    for (int ch = 0; ch < PP_COLS / 16; ++ch) {
+        uint32_t v[16];
+        sqd::tmem_ld_32x32b_x16(src + 16 * ch, v);
+        sqd::tmem_wait_ld_dep1(v);
+        if (ch + 1 == PP_COLS / 16) {
+            sqd::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) sqd::mbar_arrive_cluster(release);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sums[8 * ch + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, sums[8 * ch + i]);
+    }
+}
+
 template <bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PP_THREADS, 1)
 product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -182,7 +204,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                 const int wr = SWIGLU ? (walk.e * 2 + static_cast<int>(rank)) * p.N + tni * 128
                                       : walk.e * p.N + tni * PP_BN + static_cast<int>(rank) * 128;
                 for (int b = 0; b < kb; ++b) {
-                    if (!sqd::mbar_wait(empty(e), ph ^ 1u, abort_flag, SITE_PP_LOAD)) { ok = false; break; }
+                    if (!sqd::mbar_wait_short(empty(e), ph ^ 1u, abort_flag, SITE_PP_LOAD)) { ok = false; break; }
                     const uint32_t bar = sqd::map_to_cta(full(e), 0);
                     sqd::mbar_arrive_expect_tx_cluster(bar, PP_STAGE);
                     sqd::tma_load_2d_pair(stage(e), &tm_x, bar, b * BLK, xr);
@@ -209,8 +231,8 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                     if ((g & 1u) == r) {
                         const uint64_t ad = desc0 + static_cast<uint64_t>(e * (PP_STAGE >> 4));
                         const uint64_t bd = ad + (128 * 128 >> 4);
-                        if (!sqd::mbar_wait(full(e), ph, abort_flag, SITE_PP_MMA) ||
-                            !sqd::mbar_wait(acc_empty(r), free_ph, abort_flag, SITE_PP_ACC)) { ok = false; break; }
+                        if (!sqd::mbar_wait_short(full(e), ph, abort_flag, SITE_PP_MMA) ||
+                            !sqd::mbar_wait_short(acc_empty(r), free_ph, abort_flag, SITE_PP_ACC)) { ok = false; break; }
                         sqd::tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < 4; ++k) sqd::mma_f8_pair(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
@@ -263,62 +285,65 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         auto meet = [&]() -> bool {
             __syncwarp();
             if (lane == 0) sqd::mbar_arrive(swap(quarter));
-            const bool there = sqd::mbar_wait(swap(quarter), met, abort_flag, SITE_PP_EPI);
+            const bool there = sqd::mbar_wait_short(swap(quarter), met, abort_flag, SITE_PP_EPI);
             met ^= 1u;
             return there;
+        };
+        int c_row0 = 0, c_end = 0, c_tni = 0;      // the current tile's place, once the next one is looked up
+        auto next_tile = [&]() {
+            c_row0 = row0;
+            c_end = row_end;
+            c_tni = tni;
+            t += pairs;
+            more = walk.seek(t);
+            if (more) open_tile();
         };
         if (more) open_tile();
         while (more) {
             float2 sums[PP_COLS / 2];
 #pragma unroll
             for (int i = 0; i < PP_COLS / 2; ++i) sums[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-            for (int b = 0; b < kb; ++b, ++g) {
-                if ((b & 3) == 0) {
-                    sc = make_float4(sx4.x * sw4.x, sx4.y * sw4.y, sx4.z * sw4.z, sx4.w * sw4.w);
-                    if (b + 4 < kb) {
-                        if (sx_p) sx4 = __ldg(sx_p + (b >> 2) + 1);
-                        if (sw_p) sw4 = __ldg(sw_p + (b >> 2) + 1);
-                    }
+            // scales of four blocks: sc, and what the next four need in flight
+            const auto four_scales = [&](int b) {
+                sc = make_float4(sx4.x * sw4.x, sx4.y * sw4.y, sx4.z * sw4.z, sx4.w * sw4.w);
+                if (b + 4 < kb) {
+                    if (sx_p) sx4 = __ldg(sx_p + (b >> 2) + 1);
+                    if (sw_p) sw4 = __ldg(sw_p + (b >> 2) + 1);
                 }
-                const float2 s2 = make_float2(sc.x, sc.x);
-                sc = make_float4(sc.y, sc.z, sc.w, 0.0f);
-                const uint32_t r = g & 1u;
-                // (a wait that gave up does not leave the loop: a second way out would cost
-                // copies of all the sums; what is added then is never stored)
-                ok = sqd::mbar_wait(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
-                sqd::tc_fence_after();
-                const uint32_t src = tl + r * PP_BN;
+            };
+            // (a wait that gave up does not leave the loops: a second way out would cost
+            // copies of all the sums; what is added then is never stored)
+            int b = 0;
+            if constexpr (!SWIGLU) {       // (by four blocks: 1 to 4 % faster; the SwiGLU form has no registers for it)
+#pragma unroll 1
+                for (; b + 4 <= kb; b += 4) {
+                    four_scales(b);
+                    const float s4[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-                for (int ch = 0; ch < PP_COLS / 16; ++ch) {
-                    uint32_t v[16];
-                    sqd::tmem_ld_32x32b_x16(src + 16 * ch, v);
-                    sqd::tmem_wait_ld_dep1(v);
-                    if (ch + 1 == PP_COLS / 16) {
-                        // everything read: the buffer goes back to the MMAs
-                        sqd::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) sqd::mbar_arrive_cluster(empty0[r]);
+                    for (int q = 0; q < 4; ++q, ++g) {
+                        ok = sqd::mbar_wait_short(acc_full(g & 1u), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
+                        add_block(sums, tl + (g & 1u) * PP_BN, s4[q], lane, empty0[g & 1u]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sums[8 * ch + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
-                                                      sums[8 * ch + i]);
                 }
             }
+#pragma unroll 1
+            for (; b < kb; ++b, ++g) {
+                if ((b & 3) == 0) four_scales(b);
+                if (SWIGLU && b + 1 == kb) next_tile();   // (while the last block's MMAs run)
+                const float sv = sc.x;
+                sc = make_float4(sc.y, sc.z, sc.w, 0.0f);
+                const uint32_t r = g & 1u;
+                ok = sqd::mbar_wait_short(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
+                add_block(sums, tl + r * PP_BN, sv, lane, empty0[r]);
+            }
             if (!ok) break;
+            if (!SWIGLU) next_tile();
             float acc[PP_COLS];
 #pragma unroll
             for (int i = 0; i < PP_COLS / 2; ++i) {
                 acc[2 * i] = sums[i].x;
                 acc[2 * i + 1] = sums[i].y;
             }
-            // the tile's place, before the next one's scales are fetched
-            const int c_row0 = row0, c_end = row_end, c_tni = tni;
-            t += pairs;
-            more = walk.seek(t);
-            if (more) open_tile();
-
             if constexpr (SWIGLU) {
                 // Gate and up warp of the same rows exchange halves: the gate warp hands over its
                 // columns 64.., the up warp its columns ..63; then 64 columns of both are here.

@@ -191,7 +191,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             tile.seek(p, MP, pre, t, lane);
             if (lane == 0) {
                 for (int i = 0; ok && i < nblk; ++i) {
-                    if (!sqd::mbar_wait(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
+                    if (!sqd::mbar_wait_short(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
                     if (t != t0 || i >= early) load_w(s, b_lo + i, tile.g * MATS * p.N + tile.tn * 128);
                     sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), (b_lo + i) * BLK, tile.m0);
                     last = s;
@@ -213,7 +213,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             for (int t = t0; ok && t < tiles; t += step) {
                 for (int i = 0; i < nblk; ++i) {
                     const uint64_t ad = desc0 + static_cast<uint64_t>(s * (C::STAGE >> 4)), bd = ad + (MATS * C::W_BYTES >> 4);
-                    if (!sqd::mbar_wait(full(s), ph, abort_flag, SITE_SB_MMA)) { ok = false; break; }
+                    if (!sqd::mbar_wait_short(full(s), ph, abort_flag, SITE_SB_MMA)) { ok = false; break; }
                     sqd::tc_fence_after();
 #pragma unroll
                     for (int mat = 0; mat < MATS; ++mat)
@@ -276,7 +276,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     if (((q + 1) << 2) < b_lo + nblk) fetch(q + 1);
                 }
-                sqd::mbar_wait(done(st), ph, abort_flag, SITE_SB_EPI);
+                sqd::mbar_wait_short(done(st), ph, abort_flag, SITE_SB_EPI);
                 sqd::tc_fence_after();
                 const float4 *tb = reinterpret_cast<const float4 *>(tq + (b & 3) * MATS * MP);
 #pragma unroll
