@@ -51,12 +51,12 @@ struct CfgSkinnyB {
     static constexpr int OFF_BAR = OFF_MAX + (SWIGLU ? 7 * MP * 4 : 0);
     static constexpr int NBAR = 3 * NST + 1;                     // full[NST] done[NST] empty[NST] drain
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;          // TMEM address, abort flag
-    static constexpr int OFF_PRE = OFF_MISC + 8;                 // first tile of each expert
-    static constexpr int smem(int G) { return OFF_PRE + 4 * (G + 1) + 768; }
+    static constexpr int OFF_PRE = OFF_MISC + 8;                 // first tile, then first row of each expert
+    static constexpr int smem(int G) { return OFF_PRE + 8 * (G + 1) + 768; }
     static_assert(STAGE % 1024 == 0, "swizzled tiles");
     static_assert(MATS * (MP / 4 + SB_MAX_SPLITS - 1) * 2048 <= NST * STAGE, "the exchanged sums fit in the ring");
     static_assert(smem(512) <= 232448, "shared memory");
-    static_assert((smem(256) + 1024) * PER_SM <= 233472 && NST * COLS <= TMEM && TMEM * PER_SM <= 512, "an SM's share");
+    static_assert((smem(128) + 1024) * PER_SM <= 233472 && NST * COLS <= TMEM && TMEM * PER_SM <= 512, "an SM's share");
 };
 
 struct SkinnyBArgs {
@@ -64,7 +64,8 @@ struct SkinnyBArgs {
     int splits;
 };
 
-// First tile of every expert, pre[0 .. G] (one warp).  An expert has a tile for
+// First tile of every expert, pre[0 .. G], and behind it their first rows [0 .. G] (one
+// warp).  An expert has a tile for
 // each MP of its rows and each 128 weight rows; its row chunks come fastest, so
 // that those that share weight rows run together.
 __device__ __forceinline__ void first_tiles(const ProductArgs &a, int mp, int lane, int32_t *pre)
@@ -80,7 +81,11 @@ __device__ __forceinline__ void first_tiles(const ProductArgs &a, int mp, int la
             const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += u;
         }
-        if (g0 + lane < a.G) pre[g0 + lane + 1] = base + sum;
+        if (g0 + lane < a.G) {
+            pre[g0 + lane + 1] = base + sum;
+            pre[a.G + 1 + g0 + lane] = static_cast<int32_t>(lo);
+            if (g0 + lane == a.G - 1) pre[2 * a.G + 1] = static_cast<int32_t>(hi);
+        }
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
 }
@@ -94,12 +99,10 @@ struct SkinnyTile {
         uint32_t who;
         while ((who = __ballot_sync(0xFFFFFFFFu, g0 + lane < a.G && t < pre[g0 + lane + 1])) == 0) g0 += 32;
         g = g0 + __ffs(who) - 1;
-        int64_t lo, hi;
-        expert_rows(a, g, lo, hi);
         const int r = t - pre[g], chunks = (pre[g + 1] - pre[g]) / a.nb;
         tn = r / chunks;
-        m0 = static_cast<int>(lo) + r % chunks * mp;
-        m_end = static_cast<int>(hi);
+        m0 = pre[a.G + 1 + g] + (r - tn * chunks) * mp;
+        m_end = pre[a.G + 2 + g];
     }
 };
 
@@ -184,22 +187,26 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
+        // (the whole warp walks along: the next tile is looked up, which takes all lanes,
+        // while the first block of this one is on its way)
         int s = 0, last = -1;
         uint32_t ph = 0, last_ph = 0;
         bool ok = true;
-        for (int t = t0; t < tiles; t += step) {
-            tile.seek(p, MP, pre, t, lane);
-            if (lane == 0) {
-                for (int i = 0; ok && i < nblk; ++i) {
-                    if (!sqd::mbar_wait_short(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
-                    if (t != t0 || i >= early) load_w(s, b_lo + i, tile.g * MATS * p.N + tile.tn * 128);
-                    sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), (b_lo + i) * BLK, tile.m0);
-                    last = s;
-                    last_ph = ph;
-                    if (++s == NST) { s = 0; ph ^= 1u; }
+        if (t0 < tiles) tile.seek(p, MP, pre, t0, lane);
+        for (int t = t0; ok && t < tiles; t += step) {
+            const int w_row = tile.g * MATS * p.N + tile.tn * 128, x_row = tile.m0;
+            for (int i = 0; i < nblk; ++i) {
+                if (!sqd::mbar_wait_short(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
+                if (lane == 0) {
+                    if (t != t0 || i >= early) load_w(s, b_lo + i, w_row);
+                    sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), (b_lo + i) * BLK, x_row);
                 }
+                __syncwarp();
+                last = s;
+                last_ph = ph;
+                if (++s == NST) { s = 0; ph ^= 1u; }
+                if (i == 0 && t + step < tiles) tile.seek(p, MP, pre, t + step, lane);
             }
-            __syncwarp();
         }
         if (!ok && last >= 0) sqd::mbar_drain(full(last), last_ph);
     } else if (warp == 1) {
