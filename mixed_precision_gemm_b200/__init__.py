@@ -459,7 +459,7 @@ def sq_select_outliers(Xc: torch.Tensor, W: torch.Tensor, nO: int, group: int, O
 # channels [rows, sq_scale_ld_fp8b(K)] (weights: per 128 x 128 block).
 def _block_device(*tensors) -> int:
     """The calls below launch on the current device (returned): every tensor has to live there."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
@@ -479,6 +479,10 @@ def _k_pad(K: int) -> int:
 
 def _s_ld(K: int) -> int:
     return (K + 511) // 512 * 4
+
+
+def _up256(n: int) -> int:
+    return (n + 255) // 256 * 256
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -560,12 +564,13 @@ def sq_linear_fp8b(X: torch.Tensor, W_8, s_w, N: int, Y: torch.Tensor, workspace
     M, K = X.shape
     if Y.shape != (M, N):
         raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
-    _check_codes(W_8, s_w, ("W_8", "s_w"), (N,), K, (-(-N // 128),))
+    _expect(W_8, "W_8", torch.uint8, N, _k_pad(K))
+    _expect(s_w, "s_w", torch.float32, -(-N // 128), _s_ld(K))
     dev = _block_device(X, W_8, s_w, Y, workspace)
     st = load().sq_linear_fp8b(X.data_ptr(), M, K, _ld(X), W_8.data_ptr(), s_w.data_ptr(), N, Y.data_ptr(), _ld(Y),
-                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _raw_stream(stream, dev))
-    _raise(st, "sq_linear_fp8b")
+                               workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+    if st != SQ_OK:
+        _raise(st, "sq_linear_fp8b")
 
 
 # Mixture of experts: routing, dispatch, the experts' products, combination.
@@ -877,7 +882,7 @@ def _scope(dev: torch.device, stream):
 
 
 def _here(dev: torch.device, stream) -> bool:
-    return stream is None and dev.index == torch.cuda.current_device()
+    return stream is None and torch.cuda.is_initialized() and dev.index == torch._C._cuda_getDevice()
 
 
 @dataclasses.dataclass
@@ -926,16 +931,16 @@ def linear_fp8b(X: torch.Tensor, pw: PreparedFP8B, out: Optional[torch.Tensor] =
     """y [M, N] = x W^T for bf16 x [M, K] and one block-scaled matrix; x is quantized on the way.
 
     The workspace is allocated per call on the stream, so calls on several streams and captured graphs share none."""
-    if not _here(X.device, stream):
-        with _scope(X.device, stream):
+    dev = X.device
+    if not _here(dev, stream):
+        with _scope(dev, stream):
             return linear_fp8b(X, pw, out)
-    _rowmajor(X, "X", torch.bfloat16)
-    M, K = X.shape
-    if K != pw.K:
-        raise ValueError(f"X: expected {pw.K} channels, got {K}")
+    if X.dim() != 2 or X.shape[1] != pw.K:
+        raise ValueError(f"X: expected [.., {pw.K}], got {tuple(X.shape)}")
+    M = X.shape[0]
     if out is None:
-        out = torch.empty(M, pw.N, dtype=torch.bfloat16, device=X.device)
-    ws = torch.empty(sq_linear_workspace_bytes_fp8b(M, K), dtype=torch.uint8, device=X.device)
+        out = X.new_empty(M, pw.N)
+    ws = torch.empty(_up256(M * _k_pad(pw.K)) + _up256(M * _s_ld(pw.K) * 4), dtype=torch.uint8, device=dev)
     sq_linear_fp8b(X, pw.W_8, pw.s_w, pw.N, out, ws)
     return out
 
@@ -962,8 +967,8 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, sco
         with _scope(dev, stream):
             return route(logits, k, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
     T = logits.shape[0]
-    ids = torch.empty(T, k, dtype=torch.int32, device=dev)
-    weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     sq_route(logits, k, ids, weights, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
     return ids, weights
 
