@@ -75,6 +75,8 @@ sq_status prepare_fp8b_impl(const void *W, int64_t G, int64_t N, int64_t K, int6
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "weight blocks launch");
 }
 
+bool few_warps(int64_t M, int64_t K) { return M * ((fp8b_s_ld(K) + 7) / 8) <= 64; }
+
 // top == 0: row r of X to row r; otherwise to the rows pos[r * top ..].
 sq_status quant_fp8b_impl(const void *X, int64_t M, int64_t K, int64_t ldx, const int32_t *pos, int64_t top, int64_t rows_out,
                           void *X_8, float *s_x, cudaStream_t stream)
@@ -91,7 +93,7 @@ sq_status quant_fp8b_impl(const void *X, int64_t M, int64_t K, int64_t ldx, cons
     SQ_TRY(device_info(di));
     // 1024 channels per warp; with a few warps' worth of them 256, and one copy of a row per
     // warp (8 copies of one token of 4096 channels: 5.8 us and 4.1 us).
-    const bool few = M * ((fp8b_s_ld(K) + 7) / 8) <= 64;
+    const bool few = few_warps(M, K);
     const int64_t tasks = M * ((fp8b_s_ld(K) * 128 + (few ? 255 : 1023)) / (few ? 256 : 1024));
     const int64_t blocks = std::min<int64_t>((tasks + sqb::QB_THREADS / 32 - 1) / (sqb::QB_THREADS / 32), 8ll * di.sms);
     const cudaError_t e = launch_k(few ? sqb::quant_kernel<1> : sqb::quant_kernel<4>,
@@ -467,8 +469,19 @@ sq_status experts_fp8b_impl(const void *X, int64_t T, int64_t H, int64_t ldx, co
     float *sx = reinterpret_cast<float *>(ws + L.off_sx), *sh = reinterpret_cast<float *>(ws + L.off_sh);
     void *Z = ws + L.off_z;
     const int64_t R = T * k;
-    SQ_TRY(dispatch_impl(ids, T, k, E, offsets, pos, stream));
-    SQ_TRY(quant_fp8b_impl(X, T, H, ldx, pos, k, R, x8, sx, stream));
+    if (R <= sqm::DQ_PAIRS && few_warps(T, H)) {
+        DevInfo di;
+        SQ_TRY(device_info(di));
+        const int64_t warps = T * ((fp8b_s_ld(H) * 128 + 255) / 256);
+        const cudaError_t e = launch_k(sqm::dispatch_quant_kernel, dim3(static_cast<unsigned>((warps + 7) / 8), static_cast<unsigned>(k)),
+                                       dim3(sqb::QB_THREADS), 0, stream, 0u, ids, static_cast<int>(T), static_cast<int>(k),
+                                       static_cast<int>(E), offsets, pos, static_cast<const uint16_t *>(X), static_cast<int>(H), ldx,
+                                       static_cast<int>(fp8b_k_pad(H)), static_cast<int>(fp8b_s_ld(H)), x8, sx);
+        if (e != cudaSuccess) return cuda_fail(e, "dispatch and quantizer launch");
+    } else {
+        SQ_TRY(dispatch_impl(ids, T, k, E, offsets, pos, stream));
+        SQ_TRY(quant_fp8b_impl(X, T, H, ldx, pos, k, R, x8, sx, stream));
+    }
     SQ_TRY(swiglu_fp8b_impl(x8, sx, offsets, R, W13_8, s_w13, E, I, H, h8, sh, stream));
     SQ_TRY(grouped_fp8b_impl(h8, sh, offsets, R, W2_8, s_w2, E, H, I, Z, H, stream));
     return combine_impl(Z, R, H, pos, weights, T, k, H, Y, ldy, stream);

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "sq_device.cuh"
+#include "sq_fp8b.cuh"
 
 namespace sqm {
 
@@ -387,6 +388,78 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
             if (i < hi) pos[i] = r;
         }
     }
+}
+
+// ---------------------------------------------------------------- dispatch and quantizer for a few tokens
+// dispatch_kernel and the block quantizer's scattered form in one launch, for up to
+// 256 pairs: every CTA counts all pairs itself (a histogram and a scan over the
+// experts), each warp takes 256 channels of one copy of one token, and CTA (0, 0)
+// writes offsets and pos.  One token of 4096 channels, 8 of 64 experts: two launches
+// 7.7 us.
+constexpr int DQ_PAIRS = 256;
+
+__global__ void __launch_bounds__(sqb::QB_THREADS) dispatch_quant_kernel(const int32_t *__restrict__ ids, int T, int top, int E,
+                                                                         int32_t *__restrict__ offsets, int32_t *__restrict__ pos,
+                                                                         const uint16_t *__restrict__ X, int K, int64_t ldx,
+                                                                         int k_pad, int s_ld, uint8_t *__restrict__ X_8,
+                                                                         float *__restrict__ s_x)
+{
+    __shared__ int32_t id[DQ_PAIRS];
+    __shared__ int32_t off[MAX_EXPERTS + 1];   // counts of expert e at e + 1, then their running sum
+    sqd::pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int pairs = T * top;
+    for (int e = tid; e <= E; e += sqb::QB_THREADS) off[e] = 0;
+    __syncthreads();
+    sqd::pdl_wait();
+    if (tid < pairs) {
+        int e = ids[tid];
+        if (e < 0 || e >= E) e = -1;
+        id[tid] = e;
+        if (e >= 0) atomicAdd(&off[e + 1], 1);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        int32_t base = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            int32_t v = e0 + lane < E ? off[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e0 + lane < E) off[e0 + lane + 1] = base + v;
+            base += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int e = tid; e <= E; e += sqb::QB_THREADS) offsets[e] = off[e];
+        if (tid < pairs) {
+            int32_t r = -1;
+            if (id[tid] >= 0) {
+                r = off[id[tid]];
+                for (int j = 0; j < tid; ++j) r += id[j] == id[tid];
+            }
+            pos[tid] = r;
+        }
+    }
+    const int segs = (s_ld * sqb::BLK + 255) / 256;
+    const int w = blockIdx.x * (sqb::QB_THREADS / 32) + (tid >> 5);
+    if (w >= T * segs) return;
+    const int t = w / segs, pair = t * top + static_cast<int>(blockIdx.y);
+    const int e = id[pair];
+    if (e < 0) return;
+    int64_t d = off[e];
+    for (int j0 = 0; j0 < pair; j0 += 32) d += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < pair && id[j0 + lane] == e));
+    const int c = (w - t * segs) * 32 + lane;
+    const uint4 v = c < (K >> 3) ? sqd::ld_nc_v4(X + t * ldx + 8 * c) : make_uint4(0, 0, 0, 0);
+    uint32_t m = sqb::absmax8(v);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const sqb::BlockScale b = sqb::block_scale(__uint_as_float(m << 16));
+    if (8 * c < k_pad) *reinterpret_cast<uint2 *>(X_8 + d * k_pad + 8 * c) = sqb::block_codes(v, b);
+    if ((lane & 15) == 0 && (c >> 4) < s_ld) s_x[d * s_ld + (c >> 4)] = b.s;
 }
 
 // ---------------------------------------------------------------- combine

@@ -398,7 +398,7 @@ def dense_mixture(x, ids, w, gate_up, down):
     return y
 
 
-@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (1, 8, 64, 1024, 512), (9, 3, 7, 264, 136), (64, 4, 16, 512, 384),
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (16, 16, 300, 136, 128), (31, 8, 11, 520, 128), (32, 8, 9, 264, 136), (33, 8, 9, 264, 136), (1, 8, 64, 1024, 512), (9, 3, 7, 264, 136), (64, 4, 16, 512, 384),
                                        (333, 3, 12, 1032, 360), (700, 2, 4, 512, 640), (40, 1, 1, 128, 128)])
 def test_experts(T, k, E, H, I):
     layer = sq.SQExperts(weights(E, 2 * I, H), weights(E, H, I, seed=2), k, scoring="sigmoid")
