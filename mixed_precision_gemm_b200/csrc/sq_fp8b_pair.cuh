@@ -287,7 +287,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
             if (lane == 0) sqd::mbar_arrive(swap(quarter));
             const bool there = sqd::mbar_wait_short(swap(quarter), met, abort_flag, SITE_PP_EPI);
             met ^= 1u;
-            return there;
+            return __all_sync(0xFFFFFFFFu, there);
         };
         int c_row0 = 0, c_end = 0, c_tni = 0;      // the current tile's place, once the next one is looked up
         auto next_tile = [&]() {
@@ -336,7 +336,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
                 ok = sqd::mbar_wait_short(acc_full(r), (g >> 1) & 1u, abort_flag, SITE_PP_EPI) && ok;
                 add_block(sums, tl + r * PP_BN, sv, lane, empty0[r]);
             }
-            if (!ok) break;
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;   // (all lanes or none)
             if (!SWIGLU) next_tile();
             float acc[PP_COLS];
 #pragma unroll

@@ -196,7 +196,8 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         for (int t = t0; ok && t < tiles; t += step) {
             const int w_row = tile.g * MATS * p.N + tile.tn * 128, x_row = tile.m0;
             for (int i = 0; i < nblk; ++i) {
-                if (!sqd::mbar_wait_short(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD)) { ok = false; break; }
+                ok = __all_sync(0xFFFFFFFFu, sqd::mbar_wait_short(empty(s), ph ^ 1u, abort_flag, SITE_SB_LOAD));
+                if (!ok) break;
                 if (lane == 0) {
                     if (t != t0 || i >= early) load_w(s, b_lo + i, w_row);
                     sqd::tma_load_2d(stage(s) + MATS * C::W_BYTES, &tm_x, full(s), (b_lo + i) * BLK, x_row);

@@ -473,3 +473,60 @@ def test_linear_is_its_two_steps(M, K, N):
     wide = torch.zeros(M, K + 16, dtype=torch.bfloat16, device=DEV)
     wide[:, 8:K + 8] = x
     assert torch.equal(sq.linear_fp8b(wide[:, 8:K + 8], pw), y)
+
+
+def test_no_tokens_and_no_experts_left():
+    E, H, I, k = 4, 136, 72, 2
+    layer = sq.SQExperts(weights(E, 2, I, H), weights(E, H, I, seed=2), k)
+    empty = torch.empty(0, H, dtype=torch.bfloat16, device=DEV)
+    assert layer(empty, torch.empty(0, E, device=DEV)).shape == (0, H)
+    x = activations(300, H)
+    y = sq.experts_fp8b(x, torch.full((300, k), -1, dtype=torch.int32, device=DEV), torch.ones(300, k, device=DEV),
+                        layer.gate_up, layer.down)
+    assert bool((y == 0).all())
+    sq.sq_check()
+
+
+def test_prepared_round_trip():
+    w = weights(200, 136)
+    pw = sq.prepare_weights_fp8b(w)
+    kept = {n: v.cpu() if torch.is_tensor(v) else v for n, v in pw.state_dict().items()}
+    again = sq.PreparedFP8B.from_state_dict(kept, DEV)
+    x = activations(20, 136)
+    assert torch.equal(sq.linear_fp8b(x, again), sq.linear_fp8b(x, pw))
+
+
+def test_weights_written_just_before():
+    """Products fetch their first weights early: a preparation right before them in the stream still counts."""
+    x = activations(4, 4096)
+    a, b = weights(1024, 4096, seed=5), weights(1024, 4096, seed=6)
+    pw = sq.prepare_weights_fp8b(a)
+    want = [sq.linear_fp8b(x, sq.prepare_weights_fp8b(w)) for w in (a, b)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        sq.sq_prepare_weights_fp8b((a, b)[i % 2], pw.W_8, pw.s_w)
+        got.append(sq.linear_fp8b(x, pw))
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+def test_refusals_on_the_gpu():
+    pw = sq.prepare_weights_fp8b(weights(64, 136))
+    x = activations(4, 136)
+    with pytest.raises(ValueError):
+        sq.linear_fp8b(x[:, :128], pw)                        # channels
+    with pytest.raises(ValueError):
+        sq.linear_fp8b(x, pw, out=torch.empty(4, 72, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(TypeError):
+        sq.linear_fp8b(x.float(), pw)
+    with pytest.raises(sq.SQError) as e:                      # a row that does not start on 16 bytes
+        sq.linear_fp8b(torch.zeros(4, 152, dtype=torch.bfloat16, device=DEV)[:, 4:140], pw)
+    assert e.value.status == sq.SQ_ERR_MISALIGNED
+    ids = torch.zeros(4, 2, dtype=torch.int64, device=DEV)
+    gu, dn = sq.prepare_weights_fp8b(weights(2, 2, 64, 136)), sq.prepare_weights_fp8b(weights(2, 136, 64))
+    with pytest.raises(TypeError):
+        sq.experts_fp8b(x, ids, torch.ones(4, 2, device=DEV), gu, dn)
+    with pytest.raises(ValueError):
+        sq.experts_fp8b(x, ids.int(), torch.ones(4, 3, device=DEV), gu, dn)
+    with pytest.raises(ValueError):
+        sq.experts_fp8b(x, ids.int(), torch.ones(4, 2, device=DEV), dn, gu)
