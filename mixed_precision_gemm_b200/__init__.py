@@ -459,9 +459,14 @@ def sq_select_outliers(Xc: torch.Tensor, W: torch.Tensor, nO: int, group: int, O
 # channels [rows, sq_scale_ld_fp8b(K)] (weights: per 128 x 128 block).
 def _block_device(*tensors) -> int:
     """The calls below launch on the current device (returned): every tensor has to live there."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    dev = -1
     for t in tensors:
-        if t.get_device() != dev:
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"tensor on {t.device}, expected a GPU's")
+        if dev < 0:
+            dev = torch._C._cuda_getDevice()
+        if d != dev:
             raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
     return dev
 
@@ -558,17 +563,21 @@ def sq_gemm_fp8b(X_8, s_x, W_8, s_w, M: int, N: int, K: int, Y: torch.Tensor, st
     _raise(st, "sq_gemm_fp8b")
 
 
-def sq_linear_fp8b(X: torch.Tensor, W_8, s_w, N: int, Y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+def sq_linear_fp8b(X: torch.Tensor, W_8, s_w, N: int, Y: torch.Tensor, workspace: torch.Tensor, stream=None,
+                   _outputs_fit=False) -> None:
     _rowmajor(X, "X", torch.bfloat16)
-    _rowmajor(Y, "Y", torch.bfloat16)
     M, K = X.shape
-    if Y.shape != (M, N):
-        raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
+    if not _outputs_fit:
+        _rowmajor(Y, "Y", torch.bfloat16)
+        if Y.shape != (M, N):
+            raise ValueError(f"Y: expected shape {(M, N)}, got {tuple(Y.shape)}")
+        _block_device(Y, workspace)
     _expect(W_8, "W_8", torch.uint8, N, _k_pad(K))
     _expect(s_w, "s_w", torch.float32, -(-N // 128), _s_ld(K))
-    dev = _block_device(X, W_8, s_w, Y, workspace)
-    st = load().sq_linear_fp8b(X.data_ptr(), M, K, _ld(X), W_8.data_ptr(), s_w.data_ptr(), N, Y.data_ptr(), _ld(Y),
-                               workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+    dev = _block_device(X, W_8, s_w)
+    st = load().sq_linear_fp8b(X.data_ptr(), M, K, _ld(X), W_8.data_ptr(), s_w.data_ptr(), N, Y.data_ptr(),
+                               N if _outputs_fit else _ld(Y), workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, dev))
     if st != SQ_OK:
         _raise(st, "sq_linear_fp8b")
 
@@ -579,22 +588,29 @@ _SCORING = {"softmax": 0, "sigmoid": 1}
 
 def sq_route(logits: torch.Tensor, k: int, ids: torch.Tensor, weights: torch.Tensor,
              bias: Optional[torch.Tensor] = None, scoring: str = "softmax", groups: int = 1, keep_groups: int = 1,
-             group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+             group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None, _outputs_fit=False) -> None:
+    half = logits.dtype == torch.bfloat16
+    if not half and logits.dtype != torch.float32:
         raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
     _rowmajor(logits, "logits")
     if scoring not in _SCORING:
         raise ValueError(f"scoring: expected one of {sorted(_SCORING)}, got {scoring!r}")
     T, E = logits.shape
-    _expect(ids, "ids", torch.int32, T, k)
-    _expect(weights, "weights", torch.float32, T, k)
+    bias_ptr = None
     if bias is not None:
         _expect(bias, "bias", torch.float32, E)
-    dev = _block_device(logits, ids, weights, *(() if bias is None else (bias,)))
-    st = load().sq_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), T, E, _ld(logits),
-                         None if bias is None else bias.data_ptr(), _SCORING[scoring], groups, keep_groups, group_top, k, int(renormalize), float(scale),
-                         ids.data_ptr(), weights.data_ptr(), _raw_stream(stream, dev))
-    _raise(st, "sq_route")
+        _block_device(bias)
+        bias_ptr = bias.data_ptr()
+    if not _outputs_fit:
+        _expect(ids, "ids", torch.int32, T, k)
+        _expect(weights, "weights", torch.float32, T, k)
+        _block_device(ids, weights)
+    dev = _block_device(logits)
+    st = load().sq_route(logits.data_ptr(), int(half), T, E, _ld(logits), bias_ptr, _SCORING[scoring], groups,
+                         keep_groups, group_top, k, int(renormalize), float(scale), ids.data_ptr(),
+                         weights.data_ptr(), _raw_stream(stream, dev))
+    if st != SQ_OK:
+        _raise(st, "sq_route")
 
 
 def sq_moe_dispatch(ids: torch.Tensor, E: int, offsets: torch.Tensor, pos: torch.Tensor, stream=None) -> None:
@@ -675,7 +691,7 @@ def sq_experts_fp8b(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W
     dev = _block_device(X, ids, weights, W13_8, s_w13, W2_8, s_w2, Y, workspace)
     st = load().sq_experts_fp8b(X.data_ptr(), T, H, _ld(X), ids.data_ptr(), weights.data_ptr(), k, W13_8.data_ptr(),
                                 s_w13.data_ptr(), W2_8.data_ptr(), s_w2.data_ptr(), E, I, Y.data_ptr(), _ld(Y),
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+                                workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     _raise(st, "sq_experts_fp8b")
 
 
@@ -938,10 +954,12 @@ def linear_fp8b(X: torch.Tensor, pw: PreparedFP8B, out: Optional[torch.Tensor] =
     if X.dim() != 2 or X.shape[1] != pw.K:
         raise ValueError(f"X: expected [.., {pw.K}], got {tuple(X.shape)}")
     M = X.shape[0]
-    if out is None:
+    ws = X.new_empty(_up256(M * _k_pad(pw.K)) + _up256(M * _s_ld(pw.K) * 4), dtype=torch.uint8)
+    if out is not None:
+        sq_linear_fp8b(X, pw.W_8, pw.s_w, pw.N, out, ws)
+    else:
         out = X.new_empty(M, pw.N)
-    ws = torch.empty(_up256(M * _k_pad(pw.K)) + _up256(M * _s_ld(pw.K) * 4), dtype=torch.uint8, device=dev)
-    sq_linear_fp8b(X, pw.W_8, pw.s_w, pw.N, out, ws)
+        sq_linear_fp8b(X, pw.W_8, pw.s_w, pw.N, out, ws, None, True)
     return out
 
 
@@ -967,9 +985,9 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, sco
         with _scope(dev, stream):
             return route(logits, k, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
     T = logits.shape[0]
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    sq_route(logits, k, ids, weights, bias, scoring, groups, keep_groups, group_top, renormalize, scale)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k)) if logits.dtype == torch.float32 else ids.new_empty((T, k), dtype=torch.float32)
+    sq_route(logits, k, ids, weights, bias, scoring, groups, keep_groups, group_top, renormalize, scale, None, True)
     return ids, weights
 
 
@@ -985,11 +1003,11 @@ def experts_fp8b(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate
     T, H = X.shape
     I = gate_up.N
     if gate_up.K != H or down.N != H or down.K != I:
-        raise ValueError(f"X [.., {H}], gate_up {gate_up.N} x {gate_up.K} and down {down.N} x {down.K} do not fit together")
+        raise ValueError(f"X [.., {H}], gate_up {gate_up.N} x {gate_up.K} and down {down.N} x {down.K} do not fit "
+                         "together")
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=X.device)
-    ws = torch.empty(sq_experts_workspace_bytes_fp8b(T, ids.shape[1], down.W_8.shape[0], H, I), dtype=torch.uint8,
-                     device=X.device)
+        out = X.new_empty(T, H)
+    ws = X.new_empty(sq_experts_workspace_bytes_fp8b(T, ids.shape[1], down.W_8.shape[0], H, I), dtype=torch.uint8)
     sq_experts_fp8b(X, ids, weights, gate_up.W_8, gate_up.s_w, down.W_8, down.s_w, I, out, ws)
     return out
 
@@ -1008,7 +1026,8 @@ class SQExperts:
             self.gate_up = prepare_weights_fp8b(gate_up.reshape(E, 2, I, H))
             self.down = prepare_weights_fp8b(down)
 
-    def __call__(self, X: torch.Tensor, logits: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    def __call__(self, X: torch.Tensor, logits: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
         if not _here(X.device, stream):
             with _scope(X.device, stream):
                 return self(X, logits, out)

@@ -218,7 +218,15 @@ sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
     SQ_TRY(device_info(di));
     // Rows per weight matrix, were they spread evenly (their counts are on the device).
     const int64_t rows = a.offsets ? (a.M + a.G - 1) / a.G : a.M;
-    if (rows > 128) return launch_pair<SWIGLU>(di, a, stream);
+    // The pair kernel's 256-row tiles win where the others would read a matrix twice
+    // or would hold one CTA with 128 rows on an SM, and there are tiles for the pairs:
+    // above 64 rows, 80 x 8192 x 57344 is 125 us against 137 us, 128 x 8192 x 16384
+    // (64 tiles) 38 us against 40 us, but 100 x 8192 x 8192 (32 tiles) 34 us against
+    // 26 us; 64 experts 4096 x 1024 of 80 rows on average 87 us against 136 us.  At 64
+    // rows 87 us against 78 us.  SwiGLU (64-row tiles at most): 96 rows 169 us against
+    // 157 us, 128 rows 176 us against 186 us.
+    if (rows > 128 || (SWIGLU ? rows > 112 : rows > 64 && a.nb * int64_t{a.G} >= 128))
+        return launch_pair<SWIGLU>(di, a, stream);
     // Rows of X per tile: all of them, or fewer where even every tile split as far as
     // it goes leaves more than half of the SMs without a CTA (77 x 1000 x 1048: 9.4 us in
     // tiles of 128 rows, 5.5 us in tiles of 32; with many tiles the larger ones are

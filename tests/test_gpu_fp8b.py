@@ -398,7 +398,8 @@ def dense_mixture(x, ids, w, gate_up, down):
     return y
 
 
-@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (16, 16, 300, 136, 128), (31, 8, 11, 520, 128), (32, 8, 9, 264, 136), (33, 8, 9, 264, 136), (1, 8, 64, 1024, 512), (9, 3, 7, 264, 136), (64, 4, 16, 512, 384),
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (16, 16, 300, 136, 128), (31, 8, 11, 520, 128), (32, 8, 9, 264, 136), (33, 8, 9, 264, 136),
+                                       (1, 8, 64, 1024, 512), (9, 3, 7, 264, 136), (64, 4, 16, 512, 384),
                                        (333, 3, 12, 1032, 360), (700, 2, 4, 512, 640), (40, 1, 1, 128, 128)])
 def test_experts(T, k, E, H, I):
     layer = sq.SQExperts(weights(E, 2 * I, H), weights(E, H, I, seed=2), k, scoring="sigmoid")
@@ -530,3 +531,31 @@ def test_refusals_on_the_gpu():
         sq.experts_fp8b(x, ids.int(), torch.ones(4, 3, device=DEV), gu, dn)
     with pytest.raises(ValueError):
         sq.experts_fp8b(x, ids.int(), torch.ones(4, 2, device=DEV), dn, gu)
+
+
+@pytest.mark.parametrize("M,K,N", [(64, 256, 16384), (65, 136, 16384), (100, 520, 16256), (100, 520, 16264),
+                                   (128, 1032, 16392), (128, 128, 20480)])
+def test_linear_where_the_kernel_changes(M, K, N):
+    pw = sq.prepare_weights_fp8b(weights(N, K))
+    x = activations(M, K)
+    xc, xs = ref.quant_rows(x)
+    check_product(sq.linear_fp8b(x, pw), *ref.product(xc, xs, pw.W_8, pw.s_w))
+
+
+@pytest.mark.parametrize("rows", [64, 65, 100, 112, 113, 128, 130])
+def test_grouped_product_where_the_kernel_changes(rows):
+    """Experts of very different sizes around the mean that picks the kernel; rows behind the last one stay."""
+    E, K, N, R = 33, 264, 520, 33 * rows
+    cuts = torch.sort(torch.randint(0, R - 4, (E - 1,), generator=gen(rows), device=DEV)).values
+    off = torch.cat([torch.zeros(1, device=DEV), cuts, torch.tensor([R - 5], device=DEV)]).int()
+    pw = sq.prepare_weights_fp8b(weights(E, N, K))
+    x = activations(R, K)
+    xc, xs = sq.quant_fp8b(x)
+    y = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    sq.sq_moe_gemm_fp8b(xc, xs, off, pw.W_8, pw.s_w, N, K, y)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if b > a:
+            check_product(y[a:b], *ref.product(xc[a:b], xs[a:b], pw.W_8[e], pw.s_w[e]))
+    assert bool((y[-5:] == 7.0).all())
+    sq.sq_check()
