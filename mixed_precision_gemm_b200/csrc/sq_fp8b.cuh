@@ -180,6 +180,9 @@ struct ProductArgs {
     uint8_t *H_8;            // SwiGLU form: codes [M, h_pad] and scales [M, h_ld]
     float *s_h;
     int h_pad, h_ld;
+    // The kernel right before this one in the stream does not write offsets, and lets
+    // its successors start only after whatever wrote them has ended.
+    bool settled;
 };
 
 // Rows of expert g, clamped to the buffers whatever the offsets hold.

@@ -269,10 +269,11 @@ sq_status product_args(sqb::ProductArgs &a, const void *X_8, const float *s_x, c
 }
 
 sq_status gemm_fp8b_impl(const void *X_8, const float *s_x, const int32_t *offsets, int64_t M, const void *W_8, const float *s_w,
-                         int64_t G, int64_t N, int64_t K, void *Y, int64_t ldy, cudaStream_t stream)
+                         int64_t G, int64_t N, int64_t K, void *Y, int64_t ldy, cudaStream_t stream, bool settled = false)
 {
     sqb::ProductArgs a;
     SQ_TRY(product_args(a, X_8, s_x, offsets, M, W_8, s_w, G, N, K));
+    a.settled = settled;
     SQ_TRY(check_ld(ldy, N, "ldy"));
     if (M == 0 || N == 0) return SQ_OK;
     SQ_TRY(check_ptr(Y, true, "Y"));
@@ -401,11 +402,12 @@ sq_status swiglu_fp8b_impl(const void *X_8, const float *s_x, const int32_t *off
 }
 
 sq_status grouped_fp8b_impl(const void *X_8, const float *s_x, const int32_t *offsets, int64_t R, const void *W_8,
-                            const float *s_w, int64_t E, int64_t N, int64_t K, void *Y, int64_t ldy, cudaStream_t stream)
+                            const float *s_w, int64_t E, int64_t N, int64_t K, void *Y, int64_t ldy, cudaStream_t stream,
+                            bool settled = false)
 {
     SQ_TRY(check_experts(E));
     if (R > 0 && N > 0) SQ_TRY(check_ptr(offsets, true, "offsets"));
-    return gemm_fp8b_impl(X_8, s_x, offsets, R, W_8, s_w, E, N, K, Y, ldy, stream);
+    return gemm_fp8b_impl(X_8, s_x, offsets, R, W_8, s_w, E, N, K, Y, ldy, stream, settled);
 }
 
 sq_status combine_impl(const void *Z, int64_t R, int64_t ldz, const int32_t *pos, const float *weights, int64_t T, int64_t k,
@@ -491,7 +493,8 @@ sq_status experts_fp8b_impl(const void *X, int64_t T, int64_t H, int64_t ldx, co
         SQ_TRY(quant_fp8b_impl(X, T, H, ldx, pos, k, R, x8, sx, stream));
     }
     SQ_TRY(swiglu_fp8b_impl(x8, sx, offsets, R, W13_8, s_w13, E, I, H, h8, sh, stream));
-    SQ_TRY(grouped_fp8b_impl(h8, sh, offsets, R, W2_8, s_w2, E, H, I, Z, H, stream));
+    // (offsets come from the dispatch, which the SwiGLU product has waited for when it lets this one start)
+    SQ_TRY(grouped_fp8b_impl(h8, sh, offsets, R, W2_8, s_w2, E, H, I, Z, H, stream, true));
     return combine_impl(Z, R, H, pos, weights, T, k, H, Y, ldy, stream);
 }
 

@@ -139,7 +139,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     constexpr int MATS = SWIGLU ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = sqd::cluster_ctarank();
-    sqd::pdl_launch_dependents();
+    if (!SWIGLU) sqd::pdl_launch_dependents();
 
     const uint32_t bar0 = sbase + PP_OFF_BAR;
     auto full = [&](int e) { return bar0 + 8u * e; };
@@ -176,6 +176,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         sqd::tmem_relinquish_pair();
     }
     sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
+    if (SWIGLU) sqd::pdl_launch_dependents();   // (here: whoever starts now finds what came before this kernel complete)
     for (int g = threadIdx.x; g <= p.G; g += PP_THREADS) {
         // growing and inside the rows, whatever the offsets hold
         int64_t o = p.offsets ? p.offsets[g] : (g ? p.M : 0);
