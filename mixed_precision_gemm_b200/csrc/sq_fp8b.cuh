@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__res
     const int j_lo = gridDim.y > 1 ? blockIdx.y : 0, j_hi = gridDim.y > 1 ? j_lo + 1 : max(top, 1);
     sqd::pdl_wait();
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * (QB_THREADS / 32) + (threadIdx.x >> 5); w < tasks; w += wpg) {
-        const int64_t r = w / segs;
+        const int64_t r = tasks <= 0xFFFFFFFFll ? static_cast<uint32_t>(w) / static_cast<uint32_t>(segs) : w / segs;
         const int c0 = static_cast<int>(w - r * segs) * (SEG / 8) + lane;
         int32_t dst = -1;                       // lane j: the row's j-th copy
         if (top > 0) {

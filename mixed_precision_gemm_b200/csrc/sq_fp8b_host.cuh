@@ -425,8 +425,11 @@ sq_status combine_impl(const void *Z, int64_t R, int64_t ldz, const int32_t *pos
     SQ_TRY(check_ptr(Y, true, "Y"));
     DevInfo di;
     SQ_TRY(device_info(di));
-    const int64_t blocks = std::min<int64_t>((T * (N / 8) + sqm::CB_THREADS - 1) / sqm::CB_THREADS, 1ll << 30);
-    const cudaError_t e = launch_k(sqm::combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(sqm::CB_THREADS), 0, stream, 0u,
+    // small blocks where they spread over more SMs
+    const int threads = T * (N / 8) <= int64_t{di.sms} * 64 ? 64 : sqm::CB_THREADS;
+    const int64_t blocks = std::min<int64_t>((T * (N / 8) + threads - 1) / threads, 1ll << 30);
+    auto kern = k <= 2 ? sqm::combine_kernel<2> : k <= 4 ? sqm::combine_kernel<4> : sqm::combine_kernel<8>;
+    const cudaError_t e = launch_k(kern, dim3(static_cast<unsigned>(blocks)), dim3(static_cast<unsigned>(threads)), 0, stream, 0u,
                                    static_cast<const uint16_t *>(Z), R, ldz, pos, weights, T, static_cast<int>(k),
                                    static_cast<int>(N), static_cast<uint16_t *>(Y), ldy);
     return e == cudaSuccess ? SQ_OK : cuda_fail(e, "combine launch");
