@@ -404,10 +404,6 @@ sq_status sq_select_outliers(const void *Xc, int64_t Mc, int64_t K, int64_t ldx,
  *   - Limits: K a multiple of 8 in [8, SQ_MAX_K], N a multiple of 8.
  * Inputs are finite.  A product of two scales is an fp32 number: below 2^-126 it
  * loses precision.  Every call is asynchronous, sq_prepare_weights_fp8b too.
- * sq_gemm_fp8b and sq_linear_fp8b may read weights while the kernels before them
- * in the stream finish: weights written by an earlier kernel are seen as long as
- * that kernel does not let its successors start early (programmatic dependent
- * launch); those of this library that write them do not.
  * ------------------------------------------------------------------------ */
 int64_t sq_k_pad_fp8b(int64_t K);     /* roundup(K, 128) codes         */
 int64_t sq_scale_ld_fp8b(int64_t K);  /* roundup(K, 512) / 128 scales  */

@@ -79,13 +79,13 @@ __global__ void __launch_bounds__(QB_THREADS) quant_kernel(const uint16_t *__res
                                                            float *__restrict__ s_x)
 {
     constexpr int SEG = 32 * CHUNKS * 8;
-    sqd::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int segs = (s_ld * BLK + SEG - 1) / SEG;
     const int64_t tasks = rows * segs;
     const int64_t wpg = static_cast<int64_t>(gridDim.x) * (QB_THREADS / 32);
     const int j_lo = gridDim.y > 1 ? blockIdx.y : 0, j_hi = gridDim.y > 1 ? j_lo + 1 : max(top, 1);
     sqd::pdl_wait();
+    sqd::pdl_launch_dependents();   // (here: whoever starts now finds what came before this kernel complete)
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * (QB_THREADS / 32) + (threadIdx.x >> 5); w < tasks; w += wpg) {
         const int64_t r = tasks <= 0xFFFFFFFFll ? static_cast<uint32_t>(w) / static_cast<uint32_t>(segs) : w / segs;
         const int c0 = static_cast<int>(w - r * segs) * (SEG / 8) + lane;
@@ -133,8 +133,7 @@ __global__ void __launch_bounds__(256) weight_blocks_kernel(const uint16_t *__re
                                                             int64_t stride_g, int k_pad, int s_ld,
                                                             uint8_t *__restrict__ W_8, float *__restrict__ s_w)
 {
-    // (no early start of the next kernel: products fetch weights before they wait for
-    // their predecessors)
+    sqd::pdl_launch_dependents();
     __shared__ uint32_t red[8];
     const int kb = blockIdx.x, nb = blockIdx.y;
     const int64_t g = blockIdx.z;
@@ -180,8 +179,8 @@ struct ProductArgs {
     uint8_t *H_8;            // SwiGLU form: codes [M, h_pad] and scales [M, h_ld]
     float *s_h;
     int h_pad, h_ld;
-    // The kernel right before this one in the stream does not write offsets, and lets
-    // its successors start only after whatever wrote them has ended.
+    // The kernel right before this one in the stream writes neither the weights nor
+    // offsets, and lets its successors start only once all before it has ended.
     bool settled;
 };
 

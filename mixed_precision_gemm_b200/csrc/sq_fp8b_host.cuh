@@ -307,7 +307,7 @@ sq_status linear_fp8b_impl(const void *X, int64_t M, int64_t K, int64_t ldx, con
     uint8_t *X_8 = static_cast<uint8_t *>(workspace);
     float *s_x = reinterpret_cast<float *>(X_8 + round_up(M * fp8b_k_pad(K), 256));
     SQ_TRY(quant_fp8b_impl(X, M, K, ldx, nullptr, 0, M, X_8, s_x, stream));
-    return gemm_fp8b_impl(X_8, s_x, nullptr, M, W_8, s_w, 1, N, K, Y, ldy, stream);
+    return gemm_fp8b_impl(X_8, s_x, nullptr, M, W_8, s_w, 1, N, K, Y, ldy, stream, true);
 }
 
 // ---------------------------------------------------------------- experts

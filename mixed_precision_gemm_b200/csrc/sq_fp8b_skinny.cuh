@@ -157,12 +157,10 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         sqd::tmem_alloc(sqd::smem_u32(tmem_slot), C::TMEM);
         sqd::tmem_relinquish();
     }
-    // The first ring of weights is fetched while the previous kernels finish, where
-    // they do not write what says which weights those are: for one matrix, and for
-    // experts where the caller says that offsets are older (ProductArgs::settled).
-    // (Weights come from sq_prepare_weights_fp8b, whose kernel lets none start before
-    // it has ended.)  Experts of 4096 x 1024 x 64, one token: 34.1 us
-    // against 35.5 us, four: 62.9 us against 65.4 us.
+    // The first ring of weights is fetched while the previous kernel finishes, where
+    // that one writes neither them nor what says which they are and has waited for
+    // whoever did (ProductArgs::settled).  Experts of 4096 x 1024 x 64, one token: 34.1
+    // us against 35.5 us, four: 62.9 us against 65.4 us.
     const int b_lo = p.kb * rank / S, nblk = p.kb * (rank + 1) / S - b_lo;
     const int t0 = static_cast<int>(blockIdx.x) / S;
     auto load_w = [&](int s, int b, int row) {
@@ -173,7 +171,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     };
     SkinnyTile tile;
     int early = 0;
-    if (warp == 0 && (p.settled || !p.offsets)) {
+    if (warp == 0 && p.settled) {
         __syncwarp();
         first_tiles(p, MP, lane, pre);
         __syncwarp();
@@ -186,7 +184,7 @@ product_skinny_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     }
     sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
     if (SWIGLU) sqd::pdl_launch_dependents();   // (here: whoever starts now finds what came before this kernel complete)
-    if (warp == 0 && p.offsets && !p.settled) first_tiles(p, MP, lane, pre);
+    if (warp == 0 && !p.settled) first_tiles(p, MP, lane, pre);
     sqd::tc_fence_before();
     __syncthreads();
     sqd::tc_fence_after();
