@@ -13,13 +13,13 @@
 // Measured on a B200 at 4096 x 8192 x 8192, cycles per block of a tile: the MMAs
 // alone 629 (operands in shared memory are read at 96 and written at 64 bytes per
 // 128-cycle MMA and clock, so shared memory bounds them, not the 512 of the
-// tensor pipe); with the sums about 850.  What the sums are made of matters:
+// tensor pipe); with the sums about 825.  What the sums are made of matters:
 //   - scalar fp32 and integer instructions take cycles from the tensor pipe (4 MMAs
 //     went from 517 to over 800 cycles beside a loop of scalar FMAs), packed ones
 //     (FFMA2) hardly do (587), so the sums are packed and free of register copies;
 //   - one issuing thread's waits and commits left the pipe idle about 460 cycles
 //     per block, so two warps issue alternate blocks;
-//   - sixteen warps of 64 columns were slower (290 us against 252 at this size).
+//   - sixteen warps of 64 columns were slower (290 us against 252 us then, 233 us now).
 //
 // Warps of each CTA: 0 loads (TMA, a ring of 128-channel blocks: 128 rows of X
 // and 128 rows of W per CTA), 1 and 2 issue the pair's MMAs (first CTA), 3 only
@@ -35,6 +35,9 @@
 // sums through shared memory, each forms 64 columns of h = silu(g) u, and with
 // the block's largest magnitude (both warps' maxima) writes their E4M3 codes: h
 // never leaves the SM in another form.
+// (64 gate and 64 up rows per CTA need no exchange of sums but two scales a block: 368
+// us against 360 us for 64 experts of 512 rows, 4096 x 1024; with a sixth ring
+// stage in the freed shared memory the same.)
 #pragma once
 
 #include <type_traits>
