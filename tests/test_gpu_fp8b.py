@@ -559,3 +559,42 @@ def test_grouped_product_where_the_kernel_changes(rows):
             check_product(y[a:b], *ref.product(xc[a:b], xs[a:b], pw.W_8[e], pw.s_w[e]))
     assert bool((y[-5:] == 7.0).all())
     sq.sq_check()
+
+
+def test_offsets_past_32_bits_linear():
+    """More than 2^32 bytes of codes of x and of Y, more than 2^31 codes of W; the last rows and columns count."""
+    M, K, N = 70016, 65536, 40064
+    w = torch.randn(256, K, device=DEV, generator=gen(4)).bfloat16().repeat(N // 256 + 1, 1)[:N]
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    rows = torch.tensor([0, 1, 32767, 32768, 65535, M - 130, M - 1], device=DEV)
+    x[rows] = activations(len(rows), K)
+    pw = sq.prepare_weights_fp8b(w)
+    del w
+    y = sq.linear_fp8b(x, pw)
+    xc, xs = ref.quant_rows(x[rows])
+    for lo in (0, (N // 2) // 128 * 128, N - 128):
+        total, mags = ref.product(xc, xs, pw.W_8[lo:lo + 128], pw.s_w[lo // 128:lo // 128 + 1])
+        check_product(y[rows, lo:lo + 128], total, mags)
+    left = torch.ones(M, dtype=torch.bool, device=DEV)
+    left[rows] = False
+    assert not bool(y[left].any())
+    sq.sq_check()
+    del x, y, pw
+    torch.cuda.empty_cache()
+
+
+def test_offsets_past_32_bits_experts():
+    """More than 2^32 codes of the pairs' rows; a token alone gives what it gives in the batch."""
+    T, k, E, H, I = 66000, 16, 16, 4096, 128
+    gu, dn = sq.prepare_weights_fp8b(weights(E, 2, I, H)), sq.prepare_weights_fp8b(weights(E, H, I, seed=2))
+    x = activations(512, H).repeat(T // 512 + 1, 1)[:T]
+    ids = torch.arange(16, dtype=torch.int32, device=DEV).repeat(T, 1)
+    w = torch.rand(T, k, device=DEV, generator=gen(7))
+    y = sq.experts_fp8b(x, ids, w, gu, dn)
+    some = torch.tensor([0, 511, 32768, 65535, T - 1], device=DEV)
+    want = dense_mixture(x[some], ids[some], w[some], gu, dn)
+    rel = ((y[some].double() - want).norm(dim=1) / want.norm(dim=1)).max().item()
+    assert rel <= 2 * HALF_BF16, rel
+    sq.sq_check()
+    del x, y, w, ids
+    torch.cuda.empty_cache()
