@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS) dispatch_kernel(const int32_t *
 // dispatch_kernel and the block quantizer's scattered form in one launch, for up to
 // 256 pairs: every CTA counts all pairs itself (a histogram and a scan over the
 // experts), each warp takes 256 channels of one copy of one token, and CTA (0, 0)
-// writes offsets and pos.  One token of 4096 channels, 8 of 64 experts: two launches
-// 7.7 us.
+// writes offsets and pos.  The experts of one token of 4096 channels, 8 of 64: 35.5 us
+// a call against 39.6 us with the two launches.
 constexpr int DQ_PAIRS = 256;
 
 __global__ void __launch_bounds__(sqb::QB_THREADS) dispatch_quant_kernel(const int32_t *__restrict__ ids, int T, int top, int E,
