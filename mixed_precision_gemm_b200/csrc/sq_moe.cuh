@@ -82,7 +82,8 @@ __device__ __forceinline__ T warp_sum(T v)
 __device__ __forceinline__ bool too_close(float a, float b) { return a - b <= 7.62939453125e-6f * fmaxf(1.0f, fmaxf(fabsf(a), fabsf(b))); }
 __device__ __forceinline__ bool too_close(double, double) { return false; }
 
-__device__ __forceinline__ float finite_logit(float l) { return l != l ? -INFINITY : fminf(l, 3.402823466e38f); }
+// (-0 + 0 is +0: the keys of the two zeros differ, and they are a tie)
+__device__ __forceinline__ float finite_logit(float l) { return l != l ? -INFINITY : fminf(l, 3.402823466e38f) + 0.0f; }
 
 __device__ __forceinline__ float load_logit(const RouteArgs &a, int64_t t, int e)
 {

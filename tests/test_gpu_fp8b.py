@@ -598,3 +598,20 @@ def test_offsets_past_32_bits_experts():
     sq.sq_check()
     del x, y, w, ids
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [3, 40, 64, 256, 512])
+@pytest.mark.parametrize("kw", ROUTES)
+def test_route_zeros_of_both_signs(E, kw, dtype):
+    """-0.0 and +0.0 are the same logit: a tie inside a group and between groups (whose best scores they may be)."""
+    kw = dict(kw)
+    if kw.pop("bias", False):
+        kw["bias"] = torch.zeros(E, device=DEV).copysign(torch.randn(E, device=DEV, generator=gen(3)))
+    if kw["k"] > E // kw.get("groups", 1) * kw.get("keep_groups", 1) or E % kw.get("groups", 1):
+        kw = dict(k=1)
+    pick = torch.randint(0, 3, (37, E), device=DEV, generator=gen(E))
+    logits = torch.tensor([0.0, -0.0, -1.0], device=DEV)[pick].to(dtype)
+    logits[0, :3] = torch.tensor([-0.0, 0.0, -1.0], device=DEV)
+    check_route(logits, **kw)
+    check_route(-torch.zeros_like(logits), **kw)
