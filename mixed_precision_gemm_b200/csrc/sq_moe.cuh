@@ -75,12 +75,16 @@ __device__ __forceinline__ T warp_sum(T v)
     return v;
 }
 
-// A score closer than this to another one decides nothing in fp32 (relative to
-// the larger of 1 and the score): the hardware exponential of a logit (2^-22, and
-// 2^-24 of the argument's size, which e^-size outweighs), the sum of up to 512 of
-// them, the reciprocal and the bias leave less than 2^-18 on either side.
-__device__ __forceinline__ bool too_close(float a, float b) { return a - b <= 7.62939453125e-6f * fmaxf(1.0f, fmaxf(fabsf(a), fabsf(b))); }
-__device__ __forceinline__ bool too_close(double, double) { return false; }
+// Two scores whose fp32 values are this close (size: the larger magnitude) are put in
+// order in fp64.  A score is off by less than 20 u + 2^-24 |score|, u = 2^-23: of a softmax
+// value p = e^-x / S the exponential (2 u and 1.2 u x, its argument's rounding 0.5 u x; times
+// p at most 2 u), the sum's terms (at most 4 u times p for up to 512 of them), its up to 20
+// additions (10 u) and the quotient (2.5 u); of a sigmoid value 4 u; half a step for the bias.
+// The two sides of a comparison come to 41 u max(1, size), taken as 64 u = 2^-17.
+// A group's sum of two scores has the errors of both, and the rounding of the sum,
+// however small it is: size is then twice max(1, the sum of their magnitudes).
+__device__ __forceinline__ bool too_close(float a, float b, float size) { return a - b <= 7.62939453125e-6f * fmaxf(1.0f, size); }
+__device__ __forceinline__ bool too_close(double, double, float) { return false; }
 
 // (-0 + 0 is +0: the keys of the two zeros differ, and they are a tie)
 __device__ __forceinline__ float finite_logit(float l) { return l != l ? -INFINITY : fminf(l, 3.402823466e38f) + 0.0f; }
@@ -136,6 +140,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], 
         // inside the group.  gkey: what the lane's group counts (0: no expert left).
         const bool by_lanes = per % V == 0 && (span & (span - 1)) == 0;
         Key gkey = 0;
+        float gsize = 0.0f;                      // the scores' magnitudes in gkey
         int group = lane;                        // whose worth gkey is
         if (by_lanes) {
             Key k1 = 0, k2 = 0;
@@ -149,11 +154,16 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], 
                 k2 = max(max(k2, o2), min(k1, o1));
                 k1 = max(k1, o1);
             }
-            if (k1) gkey = a.group_top > 1 && k2 ? key_of(value_of(k1) + value_of(k2)) : k1;
+            if (k1) {
+                const bool two = a.group_top > 1 && k2;
+                gkey = two ? key_of(value_of(k1) + value_of(k2)) : k1;
+                gsize = fabsf(static_cast<float>(value_of(k1))) + (two ? fabsf(static_cast<float>(value_of(k2))) : 0.0f);
+            }
             group = lane / span;
         } else {
             for (int g = 0; g < a.groups; ++g) {
                 T worth = 0;
+                float size = 0.0f;
                 bool some = false;
                 int skip = -1;
                 for (int n = 0; n < a.group_top; ++n) {
@@ -168,9 +178,13 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], 
                     if (top == 0) break;
                     skip = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(best == top ? at : 0x7FFFFFFF)));
                     worth += value_of(top);
+                    size += fabsf(static_cast<float>(value_of(top)));
                     some = true;
                 }
-                if (lane == g) gkey = some ? key_of(worth) : Key(0);
+                if (lane == g) {
+                    gkey = some ? key_of(worth) : Key(0);
+                    gsize = size;
+                }
             }
         }
         uint32_t open = 0;                       // bit g: group g is kept
@@ -181,7 +195,9 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], 
             if (best == 0) break;
             const T v = value_of(best);
             if (n == a.keep) {
-                if (!by_logit && too_close(last, v)) sure = false;
+                // (any group may be the one whose error crosses the border: the largest counts)
+                const float size = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(gsize)));
+                if (!by_logit && too_close(last, v, 2.0f * fmaxf(1.0f, size))) sure = false;
                 break;
             }
             const int who = __ffs(__ballot_sync(0xFFFFFFFFu, rest == best)) - 1;
@@ -204,7 +220,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&l)[V], 
         if (top == 0) break;
         if (!by_logit) {
             const T v = value_of(top);
-            if (n > 0 && too_close(last, v)) sure = false;
+            if (n > 0 && too_close(last, v, fmaxf(fabsf(static_cast<float>(last)), fabsf(static_cast<float>(v))))) sure = false;
             last = v;
         }
         if (n == a.top) break;

@@ -615,3 +615,33 @@ def test_route_zeros_of_both_signs(E, kw, dtype):
     logits[0, :3] = torch.tensor([-0.0, 0.0, -1.0], device=DEV)
     check_route(logits, **kw)
     check_route(-torch.zeros_like(logits), **kw)
+
+
+def check_route_order(logits, k, bias, groups, keep_groups, scoring="softmax"):
+    """ids against 64 bits for many tokens (group_top 2); the scores are too varied to tie."""
+    T, E = logits.shape
+    l = logits.double()
+    score = (torch.softmax(l, 1) if scoring == "softmax" else torch.sigmoid(l)) + bias.double()
+    by_group = score.view(T, groups, E // groups)
+    kept = by_group.topk(2, 2).values.sum(2).topk(keep_groups, 1).indices
+    open_ = torch.zeros(T, groups, dtype=torch.bool, device=DEV).scatter_(1, kept, True)
+    score = by_group.masked_fill(~open_.unsqueeze(2), -float("inf")).flatten(1)
+    ids, _ = sq.route(logits, k, bias=bias, scoring=scoring, groups=groups, keep_groups=keep_groups, group_top=2)
+    assert torch.equal(ids.long(), score.topk(k, 1).indices)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (512, 4), (40, 4), (96, 16)])   # groups of whole lanes, and others
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [256.0, 1000.0, 4096.0])
+def test_route_groups_whose_scores_cancel(E, groups, scoring, big):
+    """A group's two best scores are about +B and -B: its sum is small, the error of their fp32 values is not."""
+    per, T = E // groups, 16384
+    bias = torch.full((groups, per), -16 * big, device=DEV)
+    for g in range(groups):
+        a, c = torch.randperm(per, device=DEV, generator=gen(g))[:2].tolist()
+        bias[g, a], bias[g, c] = big, -big
+    if groups == 8:
+        bias[3, bias[3].abs() <= big] = 0.0      # a group whose scores are small among those that are not
+    logits = 1.5 * torch.randn(T, E, device=DEV, generator=gen(E))
+    for keep in (1, groups // 2):
+        check_route_order(logits, min(4, 2 * keep), bias.flatten().contiguous(), groups, keep, scoring)
