@@ -392,9 +392,10 @@ sq_status sq_select_outliers(const void *Xc, int64_t Mc, int64_t K, int64_t ldx,
  *
  *   - Blocks: 128 consecutive channels of a token (X), 128 x 128 entries of the
  *     weights (W); the last ones may be partial.
- *   - s = a / 448 (fp32, IEEE), a = the block's absolute maximum; a == 0 gives
- *     s = 0 and all-zero codes.  e(x) = the E4M3 code nearest to the fp32
- *     quotient x / s, ties to the even code, the sign kept.
+ *   - s = a / 448 (fp32, IEEE), a = the block's absolute maximum; s == 0 (a == 0,
+ *     or an fp32 value whose quotient rounds to 0) gives all-zero codes.  e(x) =
+ *     the E4M3 code nearest to the fp32 quotient x / s, ties to the even code, the
+ *     sign kept.
  *   - Codes: u8 [rows, k_pad], k_pad = sq_k_pad_fp8b(K), zero bytes past K.
  *     Scales: f32 [rows, s_ld] for X, [ceil(N / 128), s_ld] for W, s_ld =
  *     sq_scale_ld_fp8b(K), zero past block ceil(K / 128) - 1.

@@ -1,7 +1,8 @@
 // Block-scaled FP8: E4M3 codes with one fp32 scale for each 128 channels of a
 // token (X) or each 128 x 128 block of the weights (W).
 //
-//   s = fl(a / 448), a the block's largest magnitude; a == 0: s = 0, codes 0
+//   s = fl(a / 448), a the block's largest magnitude; s == 0 (a == 0, or fp32 values
+//   so small that the quotient rounds to 0): codes 0
 //   e(x) = the E4M3 code nearest to fl(x / s), ties to even
 //   Y[m,n] = sum_b sx[m,b] sw[n/128,b] sum_{k in block b} e(X)[m,k] e(W)[n,k]
 //
@@ -34,8 +35,8 @@ struct BlockScale {
 __device__ __forceinline__ BlockScale block_scale(float amax)
 {
     BlockScale b;
-    b.zero = amax == 0.0f;
     b.s = sqq::row_scale(amax, kTop, 1.0f / kTop);   // (0 for 0)
+    b.zero = b.s == 0.0f;   // (a bf16 magnitude over 448 is an fp32 number; one of h need not be)
     b.up = !b.zero && b.s < sqq::kTinyScale;
     const float s1 = b.up ? b.s * sqq::kUpScale : b.s;
     const float inv = b.zero ? 0.0f : __frcp_rn(s1);
@@ -213,8 +214,8 @@ __device__ __forceinline__ float2 silu_mul2(float2 g, float2 u)
 }
 
 // A block's scale and what its codes need: the scale's inverse and negative, of a
-// scale brought up by 2^64 if it is tiny (the values have to be, too).  A zero
-// block's constants take zeros of either sign to code 0.
+// scale brought up by 2^64 if it is tiny (the values have to be, too).  A block of
+// scale 0 takes its values times 0, and zeros of either sign to code 0.
 struct CodeScale {
     float s, inv, neg, up;
 };
@@ -229,7 +230,7 @@ __device__ __forceinline__ CodeScale code_scale(float amax)
     c.s = b.s;
     c.inv = b.zero ? 1.0f : __uint_as_float(inv);
     c.neg = b.zero ? -1.0f : __uint_as_float(neg);
-    c.up = b.up ? sqq::kUpScale : 1.0f;
+    c.up = b.zero ? 0.0f : b.up ? sqq::kUpScale : 1.0f;
     return c;
 }
 

@@ -645,3 +645,55 @@ def test_route_groups_whose_scores_cancel(E, groups, scoring, big):
     logits = 1.5 * torch.randn(T, E, device=DEV, generator=gen(E))
     for keep in (1, groups // 2):
         check_route_order(logits, min(4, 2 * keep), bias.flatten().contiguous(), groups, keep, scoring)
+
+
+@pytest.mark.parametrize("counts", [[16], [9] * 40, [60] * 5, [300], [129, 0, 520]])
+@pytest.mark.parametrize("I", [136, 1160])
+def test_swiglu_of_tiny_rows(counts, I):
+    """Rows whose h ends near and below the smallest fp32 number: a scale that rounds to 0 has zero codes, nothing is
+    NaN, and the rows beside them keep their values."""
+    off, R = rows_by_expert(counts)
+    E, K = len(counts), 264
+    power = torch.arange(R, device=DEV) % 12
+    x = torch.randn(R, K, device=DEV, generator=gen(1)) * torch.where(power > 0, 2.0 ** -(65.0 + power), 1.0).unsqueeze(1)
+    pw = sq.prepare_weights_fp8b(weights(E, 2, I, K))
+    xc, xs = sq.quant_fp8b(x.bfloat16())
+    hc = torch.full((R, ref.up(I, 128)), 0x33, dtype=torch.uint8, device=DEV)
+    hs = torch.full((R, ref.up(I, 512) // 128), 7.0, device=DEV)
+    sq.sq_moe_swiglu_fp8b(xc, xs, off, pw.W_8, pw.s_w, I, K, hc, hs)
+    sq.sq_check()
+    got = ref.rows64(hc, hs)[:, :I]
+    for e, n in enumerate(counts):
+        if n == 0:
+            continue
+        a = int(off[e])
+        g, gm = ref.product(xc[a:a + n], xs[a:a + n], pw.W_8[e, 0], pw.s_w[e, 0])
+        u, um = ref.product(xc[a:a + n], xs[a:a + n], pw.W_8[e, 1], pw.s_w[e, 1])
+        sg = torch.sigmoid(g)
+        h = g * sg * u
+        dh = 1.1 * ACC * gm * (u.abs() + ACC * um) + (g * sg).abs() * ACC * um + 2.0 ** -18 * h.abs()
+        dh += 2.0 ** -149 * (1 + u.abs())     # silu and h are rounded to fp32's steps
+        top = torch.nn.functional.pad(h.abs() + dh, (0, -I % 128)).view(n, -1, 128).amax(2).repeat_interleave(128, 1)[:, :I]
+        # half an E4M3 step of the value, 2^-10 of the scale at least; the scale is off by half an fp32 step, 2^-150 at
+        # least, at up to 448 times that; values up to the block's largest one
+        lim = torch.maximum(2.0 ** -4 * (h.abs() + dh), 2.0 ** -10 * top / 448) + dh + 2.0 ** -23 * top + 2 * 448 * 2.0 ** -150
+        err = (got[a:a + n] - h).abs()
+        assert bool((err <= lim).all()), "h"      # (false for NaN)
+    none = hs == 0
+    codes = hc.view(R, -1, 128)
+    assert bool((codes[none[:, :codes.shape[1]]] == 0).all()), "codes of a zero scale"
+    assert bool(none[:, 0].any()) and not bool(none[:, 0].all())
+
+
+@pytest.mark.parametrize("T", [2, 40, 700])
+def test_experts_of_tiny_tokens(T):
+    E, H, I, k = 4, 264, 136, 2
+    layer = sq.SQExperts(weights(E, 2, I, H), weights(E, H, I, seed=2), k)
+    x = activations(T, H)
+    logits = torch.randn(T, E, device=DEV, generator=gen(5))
+    want = layer(x, logits)
+    small = x.clone()
+    small[::2] *= 2.0 ** -74
+    y = layer(small, logits)
+    assert bool((y[::2].abs() <= 1e-38).all())      # (false for NaN)
+    assert torch.equal(y[1::2], want[1::2])
