@@ -524,14 +524,17 @@ def sq_prepare_weights_fp8b(W: torch.Tensor, W_8: torch.Tensor, s_w: torch.Tenso
     if W.dtype != torch.bfloat16:
         raise TypeError(f"W: expected {torch.bfloat16}, got {W.dtype}")
     N, K = W.shape[-2:]
-    W3 = W.unsqueeze(0) if W.dim() == 2 else W if W.dim() == 3 else W.view(-1, N, K)
-    if W3.stride(2) != 1:
+    if W.stride(-1) != 1:
         raise ValueError("W: expected unit inner stride")
-    G = W3.shape[0]
     _expect(W_8, "W_8", torch.uint8, *W.shape[:-1], _k_pad(K))
     _expect(s_w, "s_w", torch.float32, *W.shape[:-2], -(-N // 128), _s_ld(K))
     dev = _block_device(W, W_8, s_w)
-    st = load().sq_prepare_weights_fp8b(W3.data_ptr(), G, N, K, W3.stride(1), W3.stride(0), W_8.data_ptr(),
+    if any(W.stride(d) != W.shape[d + 1] * W.stride(d + 1) for d in range(W.dim() - 3)):
+        for w, c, s in zip(W, W_8, s_w):    # no single stride goes through all matrices
+            sq_prepare_weights_fp8b(w, c, s, stream)
+        return
+    W3 = W.flatten(0, -3) if W.dim() > 2 else W.unsqueeze(0)
+    st = load().sq_prepare_weights_fp8b(W3.data_ptr(), W3.shape[0], N, K, W3.stride(1), W3.stride(0), W_8.data_ptr(),
                                         s_w.data_ptr(), _raw_stream(stream, dev))
     _raise(st, "sq_prepare_weights_fp8b")
 

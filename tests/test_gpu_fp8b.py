@@ -697,3 +697,21 @@ def test_experts_of_tiny_tokens(T):
     y = layer(small, logits)
     assert bool((y[::2].abs() <= 1e-38).all())      # (false for NaN)
     assert torch.equal(y[1::2], want[1::2])
+
+
+def test_prepare_weights_stack_of_strided_matrices():
+    """Leading dimensions that no single stride runs through."""
+    E, I, K = 3, 200, 264
+    wide = weights(E, 2 * I + 24, K + 16)
+    w = wide[:, 8:2 * I + 8, 8:K + 8]
+    stack = w.reshape(E, 2, I, K)
+    assert stack.data_ptr() == w.data_ptr()           # a view, not a copy
+    pw, want = sq.prepare_weights_fp8b(stack), sq.prepare_weights_fp8b(stack.contiguous())
+    assert torch.equal(pw.W_8, want.W_8) and torch.equal(pw.s_w, want.s_w)
+    turned = weights(2, E, I, K).transpose(0, 1)
+    pw, want = sq.prepare_weights_fp8b(turned), sq.prepare_weights_fp8b(turned.contiguous())
+    assert torch.equal(pw.W_8, want.W_8) and torch.equal(pw.s_w, want.s_w)
+    down = weights(E, K, I, seed=2)
+    layer, same = sq.SQExperts(w, down, 2), sq.SQExperts(w.contiguous(), down, 2)
+    x, logits = activations(5, K), torch.randn(5, E, device=DEV, generator=gen(5))
+    assert torch.equal(layer(x, logits), same(x, logits))
