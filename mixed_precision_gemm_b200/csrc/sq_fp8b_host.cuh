@@ -193,13 +193,14 @@ sq_status launch_skinny_b(const DevInfo &di, const sqb::ProductArgs &a, cudaStre
     // (CTAs that share an SM by the configuration's own arithmetic; the occupancy query
     // answers one for 110 KB of shared memory where two do run, which left half of the
     // places empty: down products of 96 tokens over 64 experts 62 us, 49 us with them)
-    const int64_t places = static_cast<int64_t>(C::PER_SM) * di.sms;
+    const int64_t cta_per_sm = C::per_sm(a.G);
+    const int64_t places = cta_per_sm * di.sms;
     const int64_t at_once = a.offsets ? experts * ((a.M + experts * C::MP - 1) / (experts * C::MP)) * a.nb : tiles;
     int64_t S = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(places / at_once, sqb::SB_MAX_SPLITS), a.kb / 2));
     for (; S > 1; --S) {
         int fit = 0;
         SQ_TRY(cluster_fit(reinterpret_cast<const void *>(kern), sqb::SB_THREADS, smem, static_cast<unsigned>(S), fit));
-        if (static_cast<int64_t>(fit) * C::PER_SM >= at_once) break;   // (the query counts one CTA per SM here, too)
+        if (fit * cta_per_sm >= at_once) break;   // (the query counts one CTA per SM here, too)
     }
     const int64_t grid = S > 1 ? tiles * S : std::min(tiles, places);
     if (tiles > 0x3FFFFFFFll || grid > 0x7FFFFFFFll) return fail(SQ_ERR_UNSUPPORTED, "%lld tiles", (long long)tiles);

@@ -22,8 +22,9 @@
 // SwiGLU: whoever stores a row of X has the 128 columns of h that share a scale, and
 // writes their codes.
 //
-// Memory-bound on the weights; two CTAs fit on an SM (one where the tile is
-// large), so that one loads while the other starts or finishes.
+// Memory-bound on the weights; two CTAs fit on an SM (one where the tile is large or
+// the experts are many, CfgSkinnyB::per_sm), so that one loads while the other starts
+// or finishes.
 //
 // Roles (6 warps): 0 loads (TMA), 1 issues the MMAs, 2..5 sums and stores.
 #pragma once
@@ -34,6 +35,7 @@ namespace sqb {
 
 constexpr int SB_THREADS = 192;
 constexpr int SB_MAX_SPLITS = 8;
+constexpr int SB_SM_BYTES = 233472;   // shared memory of an SM, 1 KB of it taken for each CTA
 
 enum : unsigned { SITE_SB_LOAD = 0x701, SITE_SB_MMA = 0x702, SITE_SB_EPI = 0x703 };
 
@@ -55,8 +57,11 @@ struct CfgSkinnyB {
     static constexpr int smem(int G) { return OFF_PRE + 8 * (G + 1) + 768; }
     static_assert(STAGE % 1024 == 0, "swizzled tiles");
     static_assert(MATS * (MP / 4 + SB_MAX_SPLITS - 1) * 2048 <= NST * STAGE, "the exchanged sums fit in the ring");
+    // CTAs that share an SM: PER_SM, or one where the experts' tables take the room of the
+    // second (SwiGLU in tiles of 32 rows from 165 experts on, products in tiles of 16 from 460).
+    static constexpr int per_sm(int G) { return PER_SM * (smem(G) + 1024) <= SB_SM_BYTES ? PER_SM : 1; }
     static_assert(smem(512) <= 232448, "shared memory");
-    static_assert((smem(128) + 1024) * PER_SM <= 233472 && NST * COLS <= TMEM && TMEM * PER_SM <= 512, "an SM's share");
+    static_assert(per_sm(128) == PER_SM && NST * COLS <= TMEM && TMEM * PER_SM <= 512, "an SM's share");
 };
 
 struct SkinnyBArgs {

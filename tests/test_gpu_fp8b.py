@@ -715,3 +715,28 @@ def test_prepare_weights_stack_of_strided_matrices():
     layer, same = sq.SQExperts(w, down, 2), sq.SQExperts(w.contiguous(), down, 2)
     x, logits = activations(5, K), torch.randn(5, E, device=DEV, generator=gen(5))
     assert torch.equal(layer(x, logits), same(x, logits))
+
+
+@pytest.mark.parametrize("E", [164, 165, 256, 384, 459, 460, 512])
+@pytest.mark.parametrize("mean", [2, 9, 24])
+def test_grouped_products_of_many_experts(E, mean):
+    """Where the experts' tables leave room for one CTA on an SM and not for two."""
+    K, I = 136, 264
+    counts = torch.randint(0, 2 * mean + 1, (E,), generator=gen(E), device=DEV).tolist()
+    off, R = rows_by_expert(counts)
+    x = activations(R, K)
+    xc, xs = sq.quant_fp8b(x)
+    pw = sq.prepare_weights_fp8b(weights(E, 2, I, K))
+    y = torch.empty(R, I, dtype=torch.bfloat16, device=DEV)
+    sq.sq_moe_gemm_fp8b(xc, xs, off, pw.W_8[:, 0].contiguous(), pw.s_w[:, 0].contiguous(), I, K, y)
+    hc = torch.full((R, ref.up(I, 128)), 0x33, dtype=torch.uint8, device=DEV)
+    hs = torch.full((R, ref.up(I, 512) // 128), 7.0, device=DEV)
+    sq.sq_moe_swiglu_fp8b(xc, xs, off, pw.W_8, pw.s_w, I, K, hc, hs)
+    sq.sq_check()
+    for e, n in enumerate(counts):
+        if n:
+            a = int(off[e])
+            g, gm = ref.product(xc[a:a + n], xs[a:a + n], pw.W_8[e, 0], pw.s_w[e, 0])
+            u, um = ref.product(xc[a:a + n], xs[a:a + n], pw.W_8[e, 1], pw.s_w[e, 1])
+            check_product(y[a:a + n], g, gm)
+            check_swiglu(hc[a:a + n], hs[a:a + n], g, gm, u, um, I)
