@@ -740,3 +740,45 @@ def test_grouped_products_of_many_experts(E, mean):
             u, um = ref.product(xc[a:a + n], xs[a:a + n], pw.W_8[e, 1], pw.s_w[e, 1])
             check_product(y[a:a + n], g, gm)
             check_swiglu(hc[a:a + n], hs[a:a + n], g, gm, u, um, I)
+
+
+@pytest.mark.parametrize("M,K,N", [
+    (1, 8192, 8192), (16, 136, 128), (3, 8, 8),             # K split over clusters; one block; fewer than the ring holds
+    (16, 264, 40960), (30, 1032, 40960), (5, 128, 57344),   # persistent: several tiles a CTA, one block to nine
+    (33, 4096, 1048), (64, 264, 16384), (100, 4104, 520), (128, 384, 8192)])   # tiles of 64 and of 128 rows
+def test_early_weights_change_nothing(M, K, N):
+    """The product behind the quantizer fetches its first weights before its wait; called alone it waits first."""
+    x = activations(M, K)
+    pw = sq.prepare_weights_fp8b(weights(N, K))
+    xc, xs = sq.quant_fp8b(x)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    sq.sq_gemm_fp8b(xc, xs, pw.W_8, pw.s_w, M, N, K, y)
+    for _ in range(3):
+        assert torch.equal(sq.linear_fp8b(x, pw), y)
+
+
+def test_offsets_past_32_bits_of_distinct_weights():
+    """Blocks at the start, in the middle and at the end of more than 2^31 codes of W, none like another: each is
+    prepared as by itself and gives its own columns of more than 2^32 bytes of Y, in the products for many rows and for few."""
+    M, K, N = 60032, 65536, 40064
+    at = (0, 16384, 32768, N // 2 // 128 * 128, N - 128)
+    w = torch.randn(256, K, device=DEV, generator=gen(4)).bfloat16().repeat(N // 256 + 1, 1)[:N]
+    for i, lo in enumerate(at):
+        w[lo:lo + 128] = weights(128, K, seed=20 + i) * 2.0 ** i
+    pw = sq.prepare_weights_fp8b(w)
+    for lo in at:
+        wc, ws = ref.quant_weights(w[lo:lo + 128])
+        assert torch.equal(pw.W_8[lo:lo + 128], wc) and torch.equal(pw.s_w[lo // 128], ws[0])
+    del w
+    rows = torch.tensor([0, 1, 32768, 53000, M - 130, M - 1], device=DEV)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[rows] = activations(len(rows), K)
+    xc, xs = ref.quant_rows(x[rows])
+    many, few = sq.linear_fp8b(x, pw)[rows], sq.linear_fp8b(x[rows], pw)
+    for lo in at:
+        total, mags = ref.product(xc, xs, pw.W_8[lo:lo + 128], pw.s_w[lo // 128:lo // 128 + 1])
+        check_product(many[:, lo:lo + 128], total, mags)
+        check_product(few[:, lo:lo + 128], total, mags)
+    sq.sq_check()
+    del x, pw
+    torch.cuda.empty_cache()
