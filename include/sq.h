@@ -431,18 +431,21 @@ sq_status sq_linear_fp8b(const void *X, int64_t M, int64_t K, int64_t ldx, const
 
 /*
  * The k experts of each token.  p = softmax (sigmoid == 0) or sigmoid of the
- * token's E logits; an expert's score is p + bias[e] (p without a bias).  With
- * groups > 1 the experts form `groups` equal runs; a group counts the sum of
- * its group_top (1 or 2) best scores, and only the keep_groups best groups stay
+ * token's E logits; an expert's score is p + bias[e], in 64 bits.  With groups
+ * > 1 the experts form `groups` equal runs; a group counts the sum of its
+ * group_top (1 or 2) best scores, and only the keep_groups best groups stay
  * open.  The k best scores among the open groups are chosen, best first; ties
- * (of groups too) go to the lower index, and scores are ordered as in 64 bits.
- * weights = p of the chosen (without the bias), divided by their sum + 1e-20 if
- * renorm, times scale.
+ * (of groups too) go to the lower index.  Without a bias, and with one group or
+ * group_top == 1, the score is the logit itself (-0 equals +0): it orders as p
+ * does, but also where p is the same number in 64 bits (sigmoids of 40 and 41,
+ * softmax values that are 0).  Without a bias, and with group_top == 2, it is p.
+ * weights = p of the chosen (without the bias, fp32), divided by their sum +
+ * 1e-20 if renorm, times scale.
  *   A logit of -inf or NaN is never chosen (+inf counts as the largest finite
  * fp32 value); where fewer than k remain the ids are -1 with weight 0.
  *
  *   logits  dev f32 (logits_bf16 == 0) or bf16 [T, ldl], ldl >= E
- *   bias    dev f32 [E] or NULL
+ *   bias    dev f32 [E] or NULL; finite, or -inf for experts that come last
  *   ids     dev i32 [T, k];  weights dev f32 [T, k]
  * Limits: E <= 512, k <= 16 and at most the experts of keep_groups groups,
  * groups <= 32 dividing E.

@@ -907,7 +907,8 @@ def _here(dev: torch.device, stream) -> bool:
 @dataclasses.dataclass
 class PreparedFP8B:
     """Block-scaled FP8 weights (see sq_prepare_weights_fp8b): one matrix, or a stack of them
-    (leading dimensions of W_8 and s_w)."""
+    (leading dimensions of W_8 and s_w).  Codes [N, K] and scales [ceil(N / 128), ceil(K / 128)] from
+    elsewhere are padded with zeros on the right to these shapes; E4M3 tensors are viewed as uint8."""
     N: int
     K: int
     W_8: torch.Tensor        # uint8 [..., N, sq_k_pad_fp8b(K)]

@@ -197,10 +197,12 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int g, int64_t
     hi = min(max(static_cast<int64_t>(a.offsets[g + 1]), lo), a.M);
 }
 
-// silu(g) u of two columns with the hardware's exponential and reciprocal (about 2^-21
-// of the value, far below the 2^-12 that a product's sum is known to): one MUFU
+// silu(g) u of two columns with the hardware's exponential and reciprocal: one MUFU
 // each where expf and an exact quotient cost some 30 instructions, the rest packed.
-// e^-g = inf gives g * 0 * u = 0.
+// Off by about 2^-21 of the value near g = 0; for negative g the rounding of the
+// exponential's argument adds 0.4 |g| 2^-23 (2^-20 at -20, 2^-18 at -87), far below
+// what the products' errors, 2^-12 of their terms' magnitudes, do to it.  From
+// e^-g = 2^126 on (g = -87.3) the value is 0, of a silu below 2^-119.
 __device__ __forceinline__ float2 silu_mul2(float2 g, float2 u)
 {
     const float2 t = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));

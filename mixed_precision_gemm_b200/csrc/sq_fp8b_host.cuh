@@ -51,6 +51,8 @@ sq_status check_top(int64_t k)
 }
 
 // ---------------------------------------------------------------- quantizers
+// (one pass at the copy rate: 8192 x 8192 33.5 us, 57344 x 8192 208 us, 3 bytes an entry
+// at 6.0 and 6.8 TB/s)
 sq_status prepare_fp8b_impl(const void *W, int64_t G, int64_t N, int64_t K, int64_t ldw, int64_t stride_g, void *W_8,
                             float *s_w, cudaStream_t stream)
 {
@@ -217,7 +219,9 @@ sq_status launch_product(const sqb::ProductArgs &a, cudaStream_t stream)
 {
     DevInfo di;
     SQ_TRY(device_info(di));
-    // Rows per weight matrix, were they spread evenly (their counts are on the device).
+    // Rows per weight matrix, were they spread evenly (their counts are on the device, and
+    // M counts padding too).  The figures below are of even loads; where a few experts have
+    // most of the rows, either kernel is right and neither is chosen for them.
     const int64_t rows = a.offsets ? (a.M + a.G - 1) / a.G : a.M;
     // The pair kernel's 256-row tiles win where the others would read a matrix twice
     // or would hold one CTA with 128 rows on an SM, and there are tiles for the pairs:
@@ -496,6 +500,11 @@ sq_status experts_fp8b_impl(const void *X, int64_t T, int64_t H, int64_t ldx, co
         SQ_TRY(dispatch_impl(ids, T, k, E, offsets, pos, stream));
         SQ_TRY(quant_fp8b_impl(X, T, H, ldx, pos, k, R, x8, sx, stream));
     }
+    // Z, the experts' outputs, is bf16 like every product's Y (sq_moe_gemm_fp8b and
+    // sq_moe_combine take the same steps): one more rounding, half a step of each summand.
+    // Against 64 bits the result is off by 0.0023 of its norm, 0.0017 of that the rounding of
+    // Y itself; fp32 would write and read R * H * 2 bytes more each (4096 tokens, 8 of 64,
+    // H = 4096: 0.54 GB, 82 us at the copy rate in a call of 760 us).
     SQ_TRY(swiglu_fp8b_impl(x8, sx, offsets, R, W13_8, s_w13, E, I, H, h8, sh, stream));
     // (offsets come from the dispatch, which the SwiGLU product has waited for when it lets this one start)
     SQ_TRY(grouped_fp8b_impl(h8, sh, offsets, R, W2_8, s_w2, E, H, I, Z, H, stream, true));

@@ -181,7 +181,8 @@ product_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     sqd::pdl_wait();  // operands, offsets and outputs may belong to the previous kernel
     if (SWIGLU) sqd::pdl_launch_dependents();   // (here: whoever starts now finds what came before this kernel complete)
     for (int g = threadIdx.x; g <= p.G; g += PP_THREADS) {
-        // growing and inside the rows, whatever the offsets hold
+        // inside the rows, whatever the offsets hold (an expert that ends before it begins has
+        // no tile)
         int64_t o = p.offsets ? p.offsets[g] : (g ? p.M : 0);
         offs[g] = static_cast<int32_t>(min(max(o, int64_t(0)), p.M));
     }

@@ -17,8 +17,8 @@ constexpr int RT_WARPS = 4;
 
 // ---------------------------------------------------------------- route
 // p = softmax or sigmoid of a token's logits; an expert's score is p + bias
-// (the logit itself where that gives the same order: no bias, and groups
-// judged by one score); the best `keep` of `groups` equal groups by the sum of
+// (the logit itself where p need not be known: no bias, and groups judged by one
+// score; it also orders values of p that are the same number); the best `keep` of `groups` equal groups by the sum of
 // their group_top best scores, then the `top` best scores inside them, ties to
 // the lower index.  Weights: p at the chosen experts, over their sum + 1e-20
 // if renorm, times scale.  A logit of -inf or NaN is never chosen (+inf counts

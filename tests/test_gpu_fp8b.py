@@ -782,3 +782,27 @@ def test_offsets_past_32_bits_of_distinct_weights():
     sq.sq_check()
     del x, pw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,K", [(200, 520), (128, 512), (264, 136)])
+def test_weights_quantized_elsewhere(N, K):
+    """Codes [N, K] and scales [ceil(N / 128), ceil(K / 128)] padded to the library's shapes."""
+    pw = sq.prepare_weights_fp8b(weights(N, K))
+    codes = pw.W_8[:, :K].contiguous().view(torch.float8_e4m3fn)
+    scales = pw.s_w[:, :-(-K // 128)].contiguous()
+    pad = torch.nn.functional.pad
+    again = sq.PreparedFP8B(N, K, pad(codes.view(torch.uint8), (0, sq.sq_k_pad_fp8b(K) - K)),
+                            pad(scales, (0, sq.sq_scale_ld_fp8b(K) - scales.shape[-1])))
+    x = activations(20, K)
+    assert torch.equal(sq.linear_fp8b(x, again), sq.linear_fp8b(x, pw))
+
+
+@pytest.mark.parametrize("kw", [dict(k=4), dict(k=8, scoring="sigmoid"), dict(k=4, groups=4, keep_groups=2),
+                                dict(k=6, groups=8, keep_groups=4, group_top=2, scoring="sigmoid")])
+def test_route_bias_of_minus_infinity(kw):
+    """Experts of bias -inf come after all others, in the order of their index; a group's worth may be -inf."""
+    bias = 0.1 * torch.randn(64, device=DEV, generator=gen(9))
+    bias[torch.randperm(64, device=DEV, generator=gen(10))[:50]] = -float("inf")
+    bias[:16] = -float("inf")
+    check_route(1.5 * torch.randn(40, 64, device=DEV, generator=gen(11)), bias=bias, **kw)
+    check_route(1.5 * torch.randn(4, 64, device=DEV, generator=gen(12)), bias=torch.full_like(bias, -float("inf")), **kw)
