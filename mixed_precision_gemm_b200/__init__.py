@@ -1022,7 +1022,7 @@ class SQExperts:
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, k: int, stream=None, **routing):
         E, H, I = down.shape
-        if gate_up.numel() != 2 * E * I * H or gate_up.shape[0] != E or gate_up.shape[-1] != H:
+        if gate_up.shape not in ((E, 2, I, H), (E, 2 * I, H)):
             raise ValueError(f"gate_up: expected [{E}, 2, {I}, {H}] or [{E}, {2 * I}, {H}], got {tuple(gate_up.shape)}")
         self.k = k
         self.routing = routing

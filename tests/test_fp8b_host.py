@@ -157,3 +157,10 @@ def test_ref_dispatch_and_route_by_hand():
     assert ids.tolist() == [[0, 2]] and torch.allclose(w, torch.tensor([[0.1, 0.5]], dtype=torch.float64))
     ids, _ = ref.route(l, 2, groups=2, keep_groups=1, group_top=2)
     assert ids.tolist() == [[2, 3]]
+
+
+@pytest.mark.parametrize("shape", [(4, 64, 2, 136), (4, 2, 136, 64), (4, 136, 128), (4, 64, 136), (8, 64, 136), (4 * 2, 64, 136)])
+def test_experts_refuse_other_layouts_of_gate_up(shape):
+    """Gate and up rows interleaved, or a matrix turned: as many entries, but not the layout that is meant."""
+    with pytest.raises(ValueError, match="gate_up: expected"):
+        sq.SQExperts(torch.empty(shape, dtype=torch.bfloat16), torch.empty(4, 136, 64, dtype=torch.bfloat16), 2)
